@@ -20,6 +20,12 @@ Entry points (same names as the C ABI):
     lrkv_status_str(code) -> str
 plus ``LayerCache`` (allocates one layer's buffers with torch) and
 ``make_workspace``.
+
+Full-rank serving beside it (``liblrkv_serve.so``, ``include/lrkv_serve.h``, ``serve.py``):
+    lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=Score(...))
+    lrkv_paged_append / lrkv_paged_read / lrkv_paged_attn(dims, cache, layer, ...)
+    lrkv_pages_reserve / _advance / _fork / _free / _copy / _compact(dims, cache, ...)
+plus ``Score``, ``PagedDims``, ``PagedCache`` and ``make_paged_workspace``.
 """
 import ctypes
 import os
@@ -28,6 +34,12 @@ from dataclasses import dataclass
 import torch
 
 from . import accounting  # noqa: F401  (host-side byte accounting)
+from .serve import (DEV_BAD_PAGE, DEV_BAD_SEQ, DEV_NO_PAGES, SERVE_LIB_PATH, PagedCache,  # noqa: F401
+                    PagedDims, Score, load_serve_library, lrkv_paged_append, lrkv_paged_attn,
+                    lrkv_paged_read, lrkv_paged_workspace_size, lrkv_pages_advance,
+                    lrkv_pages_compact, lrkv_pages_copy, lrkv_pages_fork, lrkv_pages_free,
+                    lrkv_pages_reserve, lrkv_prefill_attn, lrkv_prefill_workspace_size,
+                    make_paged_workspace)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblrkv.so")

@@ -3,33 +3,16 @@
 
 #include "../launch_util.cuh"
 #include "serve_host.cuh"
+#include "tensor_map.cuh"
 
 namespace {
 
 using namespace lrkv;
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = []() -> EncodeTiledFn {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(f);
-  }();
-  return fn;
-}
-
 // Rows [B][t][H][128] as a 4-d tensor (128, H, t, B): boxes of 64 columns x 1 head
 // x 128 tokens, 128-byte swizzle, zeros past the last token of a batch row.
 bool rows_map(CUtensorMap* map, const lrkv_bf16* base, int B, int t, int H, const int64_t (&st)[3]) {
-  EncodeTiledFn enc = encode_tiled();
+  serve::EncodeTiledFn enc = serve::encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)t, (cuuint64_t)B};
   // a stride whose extent is 1 is never used: any valid number does

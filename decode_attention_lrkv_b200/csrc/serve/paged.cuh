@@ -109,20 +109,22 @@ __device__ __forceinline__ int call_tokens(const int32_t* t_new_b, int b, int t_
 // The workspace of the paged calls, offsets in bytes.  Everything that has to be
 // zero between calls lies in front.
 constexpr int kMaxTq = 64;             // query tokens per sequence of lrkv_paged_attn
-constexpr int kAttnWarps = 8;
-constexpr int kMaxRowBlocks = 3;      // 8-row blocks that a CTA of lrkv_paged_attn holds
+constexpr int kMaxRowBlocks = 4;      // 8-row blocks that a CTA of lrkv_paged_attn holds
 constexpr int kRecFloats = kD + 2;    // a row's partial result: values, reference, sum
+// Warps of a lrkv_paged_attn CTA that holds nb blocks of 8 query rows: as many as their
+// accumulators leave registers for.
+__host__ __device__ constexpr int attn_warps(int nb) { return nb == 1 ? 16 : 8; }
 struct PagedWs {
   size_t tickets;   // int32 [ctas]: arrivals at a sequence that several CTAs share; zero between calls
   size_t claims;    // int32 [max(n_pages, B)]: who named an index first; zero between calls
   size_t ticket;    // int32 [4]: arrivals of a list call's CTAs; zero between calls
   size_t list;      // int32 [4 + 5 max(n_pages, B)]: counts, then lists of pages
-  size_t recs;      // float [ctas][2 + kAttnWarps][rows][kRecFloats]
+  size_t recs;      // float [ctas][2 + warps][rows][kRecFloats]
   size_t total;
   int ctas, rows, row_blocks;   // rows: padded rows per row block
 };
 
-// Rows of one kv head (g t_q) in blocks of up to 24, evenly, each padded to 8.
+// Rows of one kv head (g t_q) in blocks of up to 32, evenly, each padded to 8.
 inline PagedWs paged_ws(const lrkv_paged_dims& D, int t_q) {
   PagedWs L;
   L.ctas = num_sms();
@@ -140,7 +142,7 @@ inline PagedWs paged_ws(const lrkv_paged_dims& D, int t_q) {
   L.list = off;
   off = align_up(off + (4 + 5 * n) * sizeof(int32_t), 256);
   L.recs = off;
-  off = align_up(off + sizeof(float) * L.ctas * (2 + kAttnWarps) * (size_t)L.rows * kRecFloats, 256);
+  off = align_up(off + sizeof(float) * L.ctas * (2 + attn_warps(L.rows / 8)) * (size_t)L.rows * kRecFloats, 256);
   L.total = off;
   return L;
 }

@@ -22,12 +22,14 @@ bool codes_map(CUtensorMap* map, void* base, uint64_t all_rows, int rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-using Kernel = void (*)(const AttnParams);
 template <int NB>
-Kernel pick(int code, int page) {
-  if (code == LRKV_CODE_INT8)
-    return page == 16 ? attn_kernel<NB, LRKV_CODE_INT8, 16> : attn_kernel<NB, LRKV_CODE_INT8, 32>;
-  return page == 16 ? attn_kernel<NB, LRKV_CODE_E4M3, 16> : attn_kernel<NB, LRKV_CODE_E4M3, 32>;
+lrkv_status launch(const AttnParams& p, int ctas, cudaStream_t s) {
+  using C = AttnConfig<NB>;
+  auto kern = p.D.code == LRKV_CODE_INT8
+                  ? (p.D.page == 16 ? attn_kernel<NB, LRKV_CODE_INT8, 16> : attn_kernel<NB, LRKV_CODE_INT8, 32>)
+                  : (p.D.page == 16 ? attn_kernel<NB, LRKV_CODE_E4M3, 16> : attn_kernel<NB, LRKV_CODE_E4M3, 32>);
+  if (!set_smem(kern, C::kSmem)) return LRKV_ERR_CUDA;
+  return launch_pdl(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, s, p);
 }
 
 }  // namespace
@@ -54,6 +56,8 @@ lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   if (ws_bytes < L.total) return LRKV_ERR_INVALID_ARG;
   const uint64_t rows = (uint64_t)dims->n_layers * dims->n_pages * dims->Hkv * dims->page;
   if (rows >= (1ull << 31)) return LRKV_ERR_UNSUPPORTED;   // 32-bit tensor coordinates
+  const uint64_t tiles = ((uint64_t)dims->max_pages * dims->page + paged::kTile - 1) / paged::kTile;
+  if (tiles * dims->B * dims->Hkv * L.row_blocks >= (1ull << 31)) return LRKV_ERR_UNSUPPORTED;   // 32-bit tile numbers
   AttnParams p = {};
   const int box = dims->page < paged::kTile ? dims->page : paged::kTile;
   if (!codes_map(&p.map_k, cache->k, rows, box) || !codes_map(&p.map_v, cache->v, rows, box)) return LRKV_ERR_CUDA;
@@ -81,11 +85,13 @@ lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   p.row_blocks = L.row_blocks;
   p.per_block = (p.g * t_q + L.row_blocks - 1) / L.row_blocks;
   p.page_shift = dims->page == 16 ? 4 : dims->page == 32 ? 5 : dims->page == 64 ? 6 : 7;
-  Kernel kern = L.rows == 8 ? pick<1>(dims->code, dims->page)
-                            : L.rows == 16 ? pick<2>(dims->code, dims->page) : pick<3>(dims->code, dims->page);
-  if (!set_smem(kern, paged::attn_smem_bytes())) return LRKV_ERR_CUDA;
-  return launch_pdl(kern, dim3((unsigned)L.ctas), dim3(paged::kAttnThreads), paged::attn_smem_bytes(),
-                    static_cast<cudaStream_t>(stream), p);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (L.rows) {
+    case 8: return launch<1>(p, L.ctas, s);
+    case 16: return launch<2>(p, L.ctas, s);
+    case 24: return launch<3>(p, L.ctas, s);
+    default: return launch<4>(p, L.ctas, s);
+  }
 }
 
 }  // extern "C"

@@ -26,18 +26,17 @@
 // workspace, where the last to arrive at a sequence joins the records in order.
 #pragma once
 
+#include <cfloat>
+
 #include "paged.cuh"
 
 namespace lrkv {
 namespace paged {
 
-constexpr int kTile = 32;                    // tokens
-constexpr int kStages = 3;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kSideBytes = kTile * kD;       // codes of a tile's keys (or values)
-constexpr int kStageBytes = 2 * kSideBytes;
-constexpr int kWarpRing = kStages * kStageBytes;
-constexpr float kLazyMax = 8.f;              // rescale when a maximum grows by more (log2)
+constexpr int kTile = 32;                // tokens
+constexpr int kUnitBytes = kTile * kD;   // codes of a tile's keys, or of its values
+constexpr float kLazyMax = 8.f;          // rescale when a maximum grows by more (log2)
+constexpr float kShift = 1152.f;         // what is added to an int8 code when it becomes f16
 
 struct AttnParams {
   CUtensorMap map_k, map_v;   // codes as rows of 128 bytes; box {128, min(page, 32)}
@@ -58,22 +57,39 @@ struct AttnParams {
   float cap_log2;    // softcap * log2(e)
 };
 
-// A piece of a sequence's tiles that one warp has finished.
+// A segment is one sequence's tiles for one kv head and row block.  A piece of it that
+// one warp has finished, other than the whole of it:
 struct Piece {
-  long long seg;        // number of the segment's first tile; -1: none
+  int seg;              // number of the segment's first tile; -1: no piece
   int b, hr, tiles;     // sequence, kv head * row blocks + row block, tiles of the segment
 };
 
-struct AttnShared {
-  uint64_t bars[kAttnWarps][kStages];
-  float scale[kAttnWarps][kStages][4];       // keys of both halves, values of both halves
-  uint32_t missing[kAttnWarps][kStages];     // tokens of the tile without a page
-  Piece piece[kAttnWarps][2];                // an early one (workspace), the last one (ring)
-  long long prefix[kAttnThreads + 1];        // tiles of one kv head before every group of sequences
-  long long warp_sum[kAttnWarps];
-  int abort, last[2];
+template <int NB>
+struct AttnConfig {
+  static constexpr int kWarps = attn_warps(NB), kThreads = 32 * kWarps;
+  static constexpr int kUnits = NB == 1 ? 3 : NB == 4 ? 4 : 5;   // ring of a warp, in units
+  static constexpr bool kQShared = NB > 2;    // query fragments in shared memory instead of registers
+  static constexpr int kQBytes = kQShared ? NB * 2048 : 0;
+  static constexpr int kRows = 8 * NB, kRec = kRows * kRecFloats;
+  static constexpr int kWarpBytes = kUnits * kUnitBytes + kQBytes;
+  static_assert(kRec * 4 <= kWarpBytes, "a warp's last record lies in its ring");
+  struct Row2 {           // rows 2 t4 and 2 t4 + 1 of an 8-row block
+    float mul[2], slope[2], pos[2];
+    int lo[2], hi[2];
+  };
+  struct Shared {
+    uint64_t bars[kWarps][kUnits];
+    float scale[kWarps][kUnits][2];         // of both halves of a tile (equal with larger pages)
+    uint32_t missing[kWarps][kUnits];       // tokens of the tile without a page
+    Row2 row[kWarps][NB][4];
+    Piece piece[kWarps][2];                 // an early one (workspace), the last one (ring)
+    Piece open[2];                          // segments shared with other CTAs: with earlier ones, with later ones alone
+    int prefix[kThreads + 1];               // tiles of one kv head before every group of sequences
+    int warp_sum[kWarps];
+    int abort, last[2];
+  };
+  static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + sizeof(Shared) + 1024;
 };
-inline size_t attn_smem_bytes() { return (size_t)kAttnWarps * kWarpRing + sizeof(AttnShared) + 1024; }
 
 // What every warp knows of a sequence.
 struct Seq {
@@ -108,32 +124,48 @@ __device__ __forceinline__ Seq sequence(const AttnParams& p, int b, uint32_t* st
 struct Place {
   Seq s;
   int b, hr, tile;       // tile: within the segment
-  long long seg;         // number of the segment's first tile
+  int seg;               // number of the segment's first tile
 };
 
-__device__ __forceinline__ Place locate(const AttnParams& p, const AttnShared& sh, long long x, int per_thread,
-                                        int hr_n) {
-  int lo = 0, hi = kAttnThreads;   // the last group whose first tile is not behind x
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sh.prefix[mid] * hr_n <= x) lo = mid; else hi = mid;
-  }
+// prefix: tiles before every group of per_thread sequences; n groups, n + 1 entries, n % 32 == 0.
+__device__ __forceinline__ Place locate(const AttnParams& p, const int* prefix, int n, int x, int per_thread, int hr_n,
+                                        int lane) {
+  const int unit = x / hr_n, step = n / 32;      // prefix <= x / hr_n  <=>  prefix * hr_n <= x
+  const int hi = __popc(__ballot_sync(0xffffffffu, prefix[lane * step] <= unit)) - 1;
+  const int lo = __popc(__ballot_sync(0xffffffffu, lane < step && prefix[hi * step + lane] <= unit)) - 1;
+  const int group = hi * step + lo;              // the last group that starts at or before x
   Place at;
-  at.b = lo * per_thread;
-  long long before = sh.prefix[lo] * hr_n;
+  at.b = group * per_thread;
+  int before = prefix[group] * hr_n;
   uint32_t st = 0;
   for (;; ++at.b) {
     at.s = sequence(p, at.b, &st);
-    const long long all = (long long)at.s.tiles * hr_n;
+    const int all = at.s.tiles * hr_n;
     if (x < before + all || at.b + 1 >= p.D.B) break;
     before += all;
   }
-  const long long off = x - before, n = max(at.s.tiles, 1);
-  at.hr = (int)(off / n);
-  at.tile = (int)(off - at.hr * n);
-  at.seg = before + at.hr * n;
+  const int off = x - before, tiles = max(at.s.tiles, 1);
+  at.hr = off / tiles;
+  at.tile = off - at.hr * tiles;
+  at.seg = before + at.hr * tiles;
   return at;
 }
+
+// x tiles cut into n equal runs: run i is [start(i), start(i + 1)).  n < 2^15.
+struct Runs {
+  unsigned n, quot, rest;
+  float per_tile;   // runs per tile, nearly
+  __device__ __forceinline__ Runs(int x, int runs)
+      : n(runs), quot((unsigned)x / runs), rest((unsigned)x % runs), per_tile((float)runs / (float)x) {}
+  __device__ __forceinline__ int start(int i) const { return (int)(quot * i + rest * i / n); }
+  // the run that tile t lies in (x > 0)
+  __device__ __forceinline__ int of(int t) const {
+    int i = min((int)((float)t * per_tile), (int)n - 1);   // off by one at most
+    while (start(i) > t) --i;
+    while (i + 1 < (int)n && start(i + 1) <= t) ++i;
+    return i;
+  }
+};
 
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -150,11 +182,28 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Codes to f16x2 of the word's bytes (0, 2) and (1, 3), exactly.
+// Codes to f16x2 of the word's bytes (0, 1) and (2, 3), exactly; int8 codes with kShift
+// added: a byte with its sign bit flipped is code + 128, and the f16 with high byte 0x64
+// and that low byte is 1024 more.  The sums that such operands enter start from what the
+// shift adds to them, with the sign turned.  (Taking the shift off every operand instead,
+// by two more instructions per word: 205 against 193 us at 131072 tokens x 32 heads.)
+template <int CODE>
+__device__ __forceinline__ void codes_pairs(uint32_t w, uint32_t& h01, uint32_t& h23) {
+  if (CODE == LRKV_CODE_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    h01 = __byte_perm(u, 0x64646464u, 0x4140);
+    h23 = __byte_perm(u, 0x64646464u, 0x4342);
+  } else {
+    codes_f16<CODE>(w, h01, h23);
+  }
+}
+// The same of the bytes (0, 2) and (1, 3).
 template <int CODE>
 __device__ __forceinline__ void codes_evenodd(uint32_t w, uint32_t& h02, uint32_t& h13) {
   if (CODE == LRKV_CODE_INT8) {
-    s8x4_f16evenodd(w, h02, h13);
+    const uint32_t u = w ^ 0x80808080u;
+    h02 = __byte_perm(u, 0x64646464u, 0x4240);
+    h13 = __byte_perm(u, 0x64646464u, 0x4341);
   } else {
     const uint32_t r = __byte_perm(w, 0, 0x3120);
     h02 = e4m3x2_f16x2(r & 0xffffu);
@@ -162,111 +211,137 @@ __device__ __forceinline__ void codes_evenodd(uint32_t w, uint32_t& h02, uint32_
   }
 }
 
-// Brings tiles of one warp's run into its ring, one after the other.
-template <int PT>
+// Brings tiles of one warp's run into its ring: keys, values, keys, values, ...
+template <int NB, int PT>
 struct Producer {
+  using C = AttnConfig<NB>;
   Place at;
-  long long x, end;
-  int ids_at;            // tile that lane 0's ids are of
-  int id_a, id_b;        // this lane's page ids (tile ids_at + lane; both halves where PT = 16)
+  int x, end;
+  int rows_at;           // tile that lane 0's rows are of
+  int row_a, row_b;      // this lane's tile (rows_at + lane): its first row in the tensor map, and
+                         // that of its second half where PT = 16; kNotNeeded, kNoPage
+  int a, b;              // of the tile whose keys came last
+  int slot;              // ring slot of the next unit
+  bool values;           // the next unit holds values
   uint32_t status;
+  static constexpr int kNotNeeded = -1, kNoPage = -2;
 
-  __device__ __forceinline__ void load_ids(const AttnParams& p, int lane) {
-    ids_at = at.tile;
-    const int t = at.s.tile0 + at.tile + lane;     // tile of the sequence
-    id_a = id_b = -2;                              // not needed
-    const size_t row = (size_t)at.b * p.D.max_pages;
-    const long long pos = (long long)t * kTile;
-    if (pos < at.s.total) id_a = p.C.page_table[row + (size_t)(pos >> p.page_shift)];
-    if (PT == 16 && pos + 16 < at.s.total) id_b = p.C.page_table[row + (size_t)(pos >> p.page_shift) + 1];
-  }
-  __device__ __forceinline__ void begin(const AttnParams& p, const AttnShared& sh, int per_thread, int hr_n, int lane) {
-    at = locate(p, sh, x, per_thread, hr_n);
-    load_ids(p, lane);
-  }
-  // Issues the next tile into stage `st` (all lanes call it).
-  __device__ __forceinline__ void issue(const AttnParams& p, AttnShared& sh, int per_thread, int hr_n,
-                                        unsigned char* ring, int warp, int lane, int st) {
-    if (x >= end) return;
-    if (at.tile >= at.s.tiles) {
-      if (at.hr + 1 < hr_n) {          // the sequence's next head: the same pages
-        ++at.hr;
-        at.tile = 0;
-        if (ids_at != 0) load_ids(p, lane);
-      } else {
-        begin(p, sh, per_thread, hr_n, lane);
-      }
-    } else if (at.tile - ids_at >= 32) {
-      load_ids(p, lane);
+  __device__ __forceinline__ bool more() const { return values || x < end; }
+  __device__ __forceinline__ int row_of(const AttnParams& p, int id, int within) {
+    if (id < 0 || id >= p.D.n_pages) {
+      status |= LRKV_DEV_BAD_PAGE;
+      return kNoPage;
     }
-    const int src = at.tile - ids_at;
-    const int a = __shfl_sync(0xffffffffu, id_a, src);
-    const int b = PT == 16 ? __shfl_sync(0xffffffffu, id_b, src) : -2;
+    const unsigned ph = ((unsigned)p.layer * p.D.n_pages + id) * p.D.Hkv + (unsigned)at.hr / p.row_blocks;
+    return (int)((ph << p.page_shift) + within);
+  }
+  __device__ __forceinline__ void load_rows(const AttnParams& p, int lane) {
+    rows_at = at.tile;
+    const int pos = (at.s.tile0 + at.tile + lane) * kTile;
+    row_a = row_b = kNotNeeded;
+    const int* row = p.C.page_table + (size_t)at.b * p.D.max_pages + (pos >> p.page_shift);
+    if (at.tile + lane >= at.s.tiles) return;
+    if (pos < at.s.total) row_a = row_of(p, row[0], pos & (p.D.page - 1));
+    if (PT == 16 && pos + 16 < at.s.total) row_b = row_of(p, row[1], 0);
+  }
+  // Issues the next unit (all lanes call it).
+  __device__ __forceinline__ void issue(const AttnParams& p, typename C::Shared& sh, int per_thread, int hr_n,
+                                        unsigned char* ring, int warp, int lane) {
+    if (!values) {
+      if (at.tile >= at.s.tiles || at.tile - rows_at >= 32) {
+        if (at.tile >= at.s.tiles) {
+          if (at.hr + 1 < hr_n) ++at.hr, at.tile = 0;     // the sequence's next head
+          else at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
+        }
+        load_rows(p, lane);
+      }
+      a = __shfl_sync(0xffffffffu, row_a, at.tile - rows_at);
+      b = PT == 16 ? __shfl_sync(0xffffffffu, row_b, at.tile - rows_at) : kNotNeeded;
+    }
     if (lane == 0) {
-      unsigned char* dst = ring + st * kStageBytes;
-      uint64_t* bar = &sh.bars[warp][st];
-      float* sc = sh.scale[warp][st];
-      const int h = at.hr / p.row_blocks;
-      const size_t first = (size_t)p.layer * p.D.n_pages;
-      uint32_t missing = 0, bytes = 0;
-      const bool ok_a = a >= 0 && a < p.D.n_pages, ok_b = PT == 16 && b >= 0 && b < p.D.n_pages;
-      if (!ok_a) missing = PT == 16 ? 0xffffu : 0xffffffffu;
-      if (PT == 16 && !ok_b) missing |= 0xffff0000u;
-      if ((!ok_a && a != -2) || (PT == 16 && !ok_b && b != -2)) status |= LRKV_DEV_BAD_PAGE;
-      bytes = ((ok_a ? 1u : 0u) + (ok_b ? 1u : 0u)) * (2u * PT * kD);
-      sh.missing[warp][st] = missing;
-      mbar_arrive_expect_tx(bar, bytes);
-      if (ok_a) {
-        const size_t ph = (first + a) * p.D.Hkv + h;
-        const int within = PT == 16 ? 0 : ((at.s.tile0 + at.tile) * kTile) & (p.D.page - 1);
-        const int y = (int)((ph << p.page_shift) + within);
-        tma_load_2d(dst, &p.map_k, 0, y, bar);
-        tma_load_2d(dst + kSideBytes, &p.map_v, 0, y, bar);
-        cp_async4(sc, p.C.scale_k + ph);
-        cp_async4(sc + 2, p.C.scale_v + ph);
+      unsigned char* dst = ring + slot * kUnitBytes;
+      uint64_t* bar = &sh.bars[warp][slot];
+      float* sc = sh.scale[warp][slot];
+      const CUtensorMap* map = values ? &p.map_v : &p.map_k;
+      const float* scales = values ? p.C.scale_v : p.C.scale_k;
+      if (PT == 16) {
+        sh.missing[warp][slot] = (a < 0 ? 0xffffu : 0u) | (b < 0 ? 0xffff0000u : 0u);
+        mbar_arrive_expect_tx(bar, ((a >= 0 ? 1u : 0u) + (b >= 0 ? 1u : 0u)) * (PT * kD));
       } else {
-        sc[0] = sc[2] = 0.f;
+        sh.missing[warp][slot] = a < 0 ? 0xffffffffu : 0u;
+        mbar_arrive_expect_tx(bar, a >= 0 ? PT * kD : 0);
+      }
+      if (a >= 0) {
+        tma_load_2d(dst, map, 0, a, bar);
+        cp_async4(sc, scales + (a >> p.page_shift));
+      } else {
+        sc[0] = 0.f;
       }
       if (PT == 16) {
-        if (ok_b) {
-          const size_t ph = (first + b) * p.D.Hkv + h;
-          const int y = (int)(ph << p.page_shift);
-          tma_load_2d(dst + 16 * kD, &p.map_k, 0, y, bar);
-          tma_load_2d(dst + kSideBytes + 16 * kD, &p.map_v, 0, y, bar);
-          cp_async4(sc + 1, p.C.scale_k + ph);
-          cp_async4(sc + 3, p.C.scale_v + ph);
+        if (b >= 0) {
+          tma_load_2d(dst + 16 * kD, map, 0, b, bar);
+          cp_async4(sc + 1, scales + (b >> p.page_shift));
         } else {
-          sc[1] = sc[3] = 0.f;
+          sc[1] = 0.f;
         }
       }
       cp_async_arrive(bar);
     }
     __syncwarp();
-    ++at.tile;
-    ++x;
+    slot = slot + 1 == C::kUnits ? 0 : slot + 1;
+    if (values) ++at.tile, ++x;
+    values = !values;
   }
 };
+
+// d = A(16x16 f16, row) * B(16x8 f16, col) + c.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ void ldsm_x4_at(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t_at(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
 
 // Where the row `rho` (token * g + head within the group) of kv head h goes.
 __device__ __forceinline__ size_t row_offset(const AttnParams& p, int b, int h, int rho) {
   return (((size_t)b * p.t_q + rho / p.g) * p.D.Hq + h * p.g + rho % p.g) * kD;
 }
 
-// Joins n records of one row (m, l and four values from d): weights 2^(m_i - max m).
-template <typename Rec>
-__device__ __forceinline__ void join_rows(int n, Rec rec, int rows, int row, int d, float4& o, float& m, float& l) {
-  m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, rec(i)[rows * kD + row]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  l = 0.f;
+// The place of bit number i of the set bits of a mask.
+__device__ __forceinline__ int nth_bit(uint32_t mask, int i) {
+  int at = 0;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1) {
+    const int below = __popc((mask >> at) & ((1u << step) - 1u));
+    if (i >= below) i -= below, at += step;
+  }
+  return at;
+}
+// Joins row `row` of n <= 32 records by a warp, four values to a lane: weights 2^(m_i - max m).
+// Lane i holds record i's address.
+__device__ __forceinline__ void join_row(int n, const float* rec, int rows, int row, int lane, float4& o, float& m,
+                                         float& l) {
+  const float mi = lane < n ? rec[rows * kD + row] : -INFINITY, li = lane < n ? rec[rows * kD + rows + row] : 0.f;
+  m = warp_max(mi);
+  const float w = ex2(mi - (m == -INFINITY ? 0.f : m));   // 0 for lanes past n
+  l = warp_sum(w * li);
   o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < n; ++i) {
-    const float* r = rec(i);
-    const float w = ex2(r[rows * kD + row] - ref);
-    const float4 v = *reinterpret_cast<const float4*>(r + row * kD + d);
-    l = fmaf(w, r[rows * kD + rows + row], l);
-    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    const float* ri = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec), i));
+    const float4 v = *reinterpret_cast<const float4*>(ri + row * kD + 4 * lane);
+    o.x = fmaf(wi, v.x, o.x), o.y = fmaf(wi, v.y, o.y), o.z = fmaf(wi, v.z, o.z), o.w = fmaf(wi, v.w, o.w);
   }
 }
 __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, float l) {
@@ -277,25 +352,27 @@ __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, floa
 
 // NB: blocks of 8 query rows; CODE: LRKV_CODE_*; PT: tokens of a tile on one page (16 or 32).
 template <int NB, int CODE, int PT>
-__global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = AttnConfig<NB>;
+  constexpr int W = C::kWarps, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kD], references, sums
+  constexpr bool kInt = CODE == LRKV_CODE_INT8;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  AttnShared& sh = *reinterpret_cast<AttnShared*>(sm + kAttnWarps * kWarpRing);
-  constexpr int ROWS = 8 * NB;
-  constexpr int kRec = ROWS * kRecFloats;   // floats of a record: values [ROWS][kD], references, sums
-  static_assert(kRec * 4 <= kWarpRing, "a warp's last record lies in its ring");
+  // rings first: their units are 1024-aligned
+  typename C::Shared& sh = *reinterpret_cast<typename C::Shared*>(sm + W * C::kWarpBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int hr_n = p.D.Hkv * p.row_blocks;
-  const int per_thread = (p.D.B + kAttnThreads - 1) / kAttnThreads;
+  const int per_thread = (p.D.B + C::kThreads - 1) / C::kThreads;
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&sh.bars[warp][s], 2);
+    for (int s = 0; s < C::kUnits; ++s) mbar_init(&sh.bars[warp][s], 2);
     fence_mbar_init();
     sh.piece[warp][0].seg = sh.piece[warp][1].seg = -1;
   }
   if (tid == 0) {
     sh.abort = 0;
+    sh.open[0].seg = sh.open[1].seg = -1;
     tc5::prefetch_tensormap(&p.map_k);
     tc5::prefetch_tensormap(&p.map_v);
   }
@@ -305,61 +382,90 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   // tiles of one kv head and row block before every thread's sequences
   uint32_t status = 0;
   {
-    long long n = 0;
+    int n = 0;
     const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.D.B);
     for (int b = b0; b < b1; ++b) n += sequence(p, b, &status).tiles;
     if (blockIdx.x != 0) status = 0;   // one CTA reports
-    long long sum = n;
+    int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
     if (lane == 31) sh.warp_sum[warp] = sum;
     __syncthreads();
-    long long before = 0;
+    int before = 0;
     for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
     sh.prefix[tid + 1] = before + sum;
     if (tid == 0) sh.prefix[0] = 0;
     __syncthreads();
   }
-  const long long T = sh.prefix[kAttnThreads] * hr_n;
-  const long long ctas = min((long long)gridDim.x, (T + kAttnWarps - 1) / kAttnWarps);   // a tile per warp at least
-  if (blockIdx.x >= ctas) {
+  const int T = sh.prefix[C::kThreads] * hr_n;
+  const int ctas = min((int)gridDim.x, (T + W - 1) / W);   // a tile per warp at least
+  if ((int)blockIdx.x >= ctas) {
     if (status) atomicOr(p.C.dev_status, status);
     return;
   }
-  const long long X0 = T * blockIdx.x / ctas, X1 = T * (blockIdx.x + 1) / ctas;
-  const long long worker = (long long)blockIdx.x * kAttnWarps + warp, workers = ctas * kAttnWarps;
-  unsigned char* ring = sm + warp * kWarpRing;
+  const Runs workers(T, ctas * W);
+  const int X0 = workers.start(blockIdx.x * W), X1 = workers.start((blockIdx.x + 1) * W);
+  unsigned char* ring = sm + warp * C::kWarpBytes;
+  uint2* q_sh = reinterpret_cast<uint2*>(ring + C::kUnits * kUnitBytes);
 
-  Producer<PT> prod;
-  prod.x = T * worker / workers;
-  prod.end = T * (worker + 1) / workers;
+  Producer<NB, PT> prod;
+  prod.x = workers.start(blockIdx.x * W + warp);
+  prod.end = workers.start(blockIdx.x * W + warp + 1);
+  prod.slot = 0;
+  prod.values = false;
   prod.status = 0;
-  long long x = prod.x;
-  const long long end = prod.end;
-  int issued = 0, used = 0;
+  int x = prod.x;
+  const int end = prod.end;
+  int slot = 0;
+  uint32_t phase = 0;
   bool ok = true;
+  Place at;
   if (x < end) {
-    prod.begin(p, sh, per_thread, hr_n, lane);
+    at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
+    prod.at = at;
+    prod.load_rows(p, lane);
 #pragma unroll 1
-    for (int s = 0; s < kStages && prod.x < end; ++s, ++issued)
-      prod.issue(p, sh, per_thread, hr_n, ring, warp, lane, s);
+    for (int s = 0; s < C::kUnits && prod.more(); ++s) prod.issue(p, sh, per_thread, hr_n, ring, warp, lane);
   }
+  int in_flight = min(C::kUnits, 2 * (end - x));
+  // Waits for the next unit; on a time-out leaves no copy in flight.
+  auto wait_unit = [&]() {
+    if (!ok) return false;
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.bars[warp][slot], phase, kWaitIters));
+    if (!ok) {
+      if (lane == 0) sh.abort = 1;
+      for (int i = 1; i < in_flight; ++i) {
+        const int s = slot + i;
+        mbar_wait_bounded(&sh.bars[warp][s % C::kUnits], phase ^ (s >= C::kUnits), kWaitIters);
+      }
+    }
+    return ok;
+  };
+  // The unit has been read: bring the next one into its slot.
+  auto next_unit = [&]() {
+    slot = slot + 1 == C::kUnits ? 0 : slot + 1;
+    phase ^= slot == 0;
+    __syncwarp();
+    if (prod.more()) prod.issue(p, sh, per_thread, hr_n, ring, warp, lane);
+    else --in_flight;
+  };
 
-  while (x < end) {
-    const Place at = locate(p, sh, x, per_thread, hr_n);
+  for (bool first = true; x < end; first = false) {
+    if (!first) at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
     const int h = at.hr / p.row_blocks, rb = at.hr % p.row_blocks;
-    const int n_tiles = (int)min((long long)(at.s.tiles - at.tile), end - x);
+    const int n_tiles = min(at.s.tiles - at.tile, end - x);
     const int rho0 = rb * p.per_block, rho1 = min(min(rho0 + p.per_block, p.g * p.t_q), p.g * at.s.n_rows);
 
     // queries of the block as B fragments, scaled by a power of two per row so that the
     // row's largest element lies in [2^14, 2^15): f16 then keeps what is above 2^-28 of it
-    uint32_t qf[NB][8][2];
-    float mul[NB][2], m[NB][2], l[NB][2], slope[NB][2];
-    int lo[NB][2], hi[NB][2], pos[NB][2];
+    uint32_t qf[C::kQShared ? 1 : NB][8][2];
+    float m[NB][2], l[NB][2], s0[NB][2];   // s0: what the sums of keys' products start from
     int all_lo = 0, all_hi = 0x7fffffff;   // keys that every row sees
+    const uint32_t minus_shift[4] = {0xE480E480u, 0xE480E480u, 0xE480E480u, 0xE480E480u};   // f16x2 (-1152, -1152)
+    __syncwarp();
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int rho = rho0 + 8 * nb + g8;
@@ -381,24 +487,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
       // 2^(14 - e) as two factors that are normal in fp32
       const int up = 14 - e, up_a = up / 2;
       const float fa = __uint_as_float((uint32_t)(127 + up_a) << 23), fb = __uint_as_float((uint32_t)(127 + up - up_a) << 23);
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        qf[nb][c][0] = cvt_f16x2(bf_lo(w[c].x) * fa * fb, bf_hi(w[c].x) * fa * fb);
-        qf[nb][c][1] = cvt_f16x2(bf_lo(w[c].y) * fa * fb, bf_hi(w[c].y) * fa * fb);
+        const uint32_t b0 = cvt_f16x2(bf_lo(w[c].x) * fa * fb, bf_hi(w[c].x) * fa * fb);
+        const uint32_t b1 = cvt_f16x2(bf_lo(w[c].y) * fa * fb, bf_hi(w[c].y) * fa * fb);
+        if (kInt) mma_f16(acc, minus_shift, b0, b1, acc);
+        if (C::kQShared) q_sh[(c * NB + nb) * 32 + lane] = make_uint2(b0, b1);
+        else qf[C::kQShared ? 0 : nb][c][0] = b0, qf[C::kQShared ? 0 : nb][c][1] = b1;
       }
-      // this thread's score columns are rows 2 t4, 2 t4 + 1: their exponents come from lanes of those rows
+      // this thread's score columns are rows 2 t4, 2 t4 + 1; lane t4 keeps what is known of them
+      typename C::Row2 row;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        s0[nb][j] = acc[j];
         const int er = __shfl_sync(0xffffffffu, e, (2 * t4 + j) * 4);
         const int down = er - 14, da = down / 2;
-        mul[nb][j] = p.row_log2 * __uint_as_float((uint32_t)(127 + da) << 23) * __uint_as_float((uint32_t)(127 + down - da) << 23);
+        row.mul[j] = p.row_log2 * __uint_as_float((uint32_t)(127 + da) << 23) * __uint_as_float((uint32_t)(127 + down - da) << 23);
         const int r = rho0 + 8 * nb + 2 * t4 + j;
         m[nb][j] = -INFINITY;
         l[nb][j] = 0.f;
-        lo[nb][j] = 0;
-        hi[nb][j] = 0x7fffffff;
-        pos[nb][j] = 0;
-        slope[nb][j] = 0.f;
+        row.lo[j] = 0;
+        row.hi[j] = 0x7fffffff;
+        row.pos[j] = row.slope[j] = 0.f;
         if (r < rho1) {
           const int tok = r / p.g;
           const size_t meta = (size_t)at.b * p.t_q + tok;
@@ -411,15 +522,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           }
           z = min(z, at.s.total - 1);
           if (a > z) a = 0x7fffffff, z = -1;
-          lo[nb][j] = a;
-          hi[nb][j] = z;
-          pos[nb][j] = i;
-          if (p.slopes) slope[nb][j] = p.slopes[h * p.g + r % p.g] * kLog2e;
+          row.lo[j] = a;
+          row.hi[j] = z;
+          row.pos[j] = (float)i;
+          if (p.slopes) row.slope[j] = p.slopes[h * p.g + r % p.g] * kLog2e;
           all_lo = max(all_lo, a);
           all_hi = min(all_hi, z);
         }
       }
+      if (g8 == 0) sh.row[warp][nb][t4] = row;
     }
+    __syncwarp();
     all_lo = __reduce_max_sync(0xffffffffu, all_lo);
     all_hi = __reduce_min_sync(0xffffffffu, all_hi);
 
@@ -432,33 +545,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k) o[nb][dt][k] = 0.f;
 
 #pragma unroll 1
-    for (int it = 0; it < n_tiles && ok; ++it) {
-      const int st = used % kStages;
+    for (int it = 0; it < n_tiles; ++it) {
       const int base = (at.s.tile0 + at.tile + it) * kTile;
-      bool got = mbar_wait_bounded(&sh.bars[warp][st], (used / kStages) & 1, kWaitIters);
-      got = __all_sync(0xffffffffu, got);
-      if (!got) {   // the results are void, but the joins below still take place
-        ok = false;
-        if (lane == 0) sh.abort = 1;
-        for (int i = used + 1; i < issued; ++i)   // leave no copy in flight
-          mbar_wait_bounded(&sh.bars[warp][i % kStages], (i / kStages) & 1, kWaitIters);
-        break;
-      }
-      unsigned char* kt = ring + st * kStageBytes;
-      unsigned char* vt = kt + kSideBytes;
-      const float sk0 = sh.scale[warp][st][0], sk1 = PT == 16 ? sh.scale[warp][st][1] : sk0;
-      const float sv0 = sh.scale[warp][st][2], sv1 = PT == 16 ? sh.scale[warp][st][3] : sv0;
-      uint32_t gone = sh.missing[warp][st];
+      if (!wait_unit()) break;   // the results are void, but the joins below still take place
+      const uint32_t kt = smem_u32(ring + slot * kUnitBytes) + (lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4);
+      const float sk0 = sh.scale[warp][slot][0], sk1 = PT == 16 ? sh.scale[warp][slot][1] : sk0;
+      uint32_t gone = sh.missing[warp][slot];   // tokens that are not there
       const int valid = at.s.total - base;
       if (valid < kTile) gone |= valid <= 0 ? 0xffffffffu : 0xffffffffu << valid;
-      if (gone) {   // what lies there may be NaN, which a zero weight keeps: clear those value rows
-        if (gone >> lane & 1) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vt + lane * kD + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
 
       float s[NB][2][4];
 #pragma unroll
@@ -466,47 +560,81 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[nb][mt][k] = 0.f;
+          for (int k = 0; k < 4; ++k) s[nb][mt][k] = kInt ? s0[nb][k & 1] : 0.f;
 #pragma unroll
-      for (int c = 0; c < 8; c += 2)
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t a[2][2][4];   // [16 dims][16 tokens]
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
-          const int row = mt * 16 + (lane & 15);
-          uint32_t r[4], a[2][4];
-          ldsm_x4(r[0], r[1], r[2], r[3], kt + row * kD + (((c + (lane >> 4)) ^ (row & 7)) << 4));
-          codes_f16<CODE>(r[0], a[0][0], a[0][2]);
-          codes_f16<CODE>(r[1], a[0][1], a[0][3]);
-          codes_f16<CODE>(r[2], a[1][0], a[1][2]);
-          codes_f16<CODE>(r[3], a[1][1], a[1][3]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-              mma_16816_f16(s[nb][mt], a[i][0], a[i][1], a[i][2], a[i][3], qf[nb][c + i][0], qf[nb][c + i][1]);
+          uint32_t r[4];
+          ldsm_x4_at(r, (kt ^ (c << 4)) + mt * 16 * kD);
+          codes_pairs<CODE>(r[0], a[0][mt][0], a[0][mt][2]);
+          codes_pairs<CODE>(r[1], a[0][mt][1], a[0][mt][3]);
+          codes_pairs<CODE>(r[2], a[1][mt][0], a[1][mt][2]);
+          codes_pairs<CODE>(r[3], a[1][mt][1], a[1][mt][3]);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            uint2 b;
+            if (C::kQShared) b = q_sh[((c + i) * NB + nb) * 32 + lane];
+            else b = make_uint2(qf[C::kQShared ? 0 : nb][c + i][0], qf[C::kQShared ? 0 : nb][c + i][1]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+              mma_f16(s[nb][mt], a[i][mt], b.x, b.y, s[nb][mt]);
+          }
+      }
+      next_unit();
 
       const bool whole = base >= all_lo && base + kTile - 1 <= all_hi && gone == 0;
-      float mx[NB][2];
+      // weights are 2^(f s - m): the factor f of raw products is 1 once a modifier has been applied
+      float mx[NB][2], f[NB][PT == 16 ? 2 : 1][2];
       bool grow = false;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
+        const typename C::Row2& row = sh.row[warp][nb][t4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float f0 = sk0 * mul[nb][j], f1 = PT == 16 ? sk1 * mul[nb][j] : f0;
-          mx[nb][j] = -INFINITY;
+          f[nb][0][j] = fmaxf(sk0 * row.mul[j], FLT_MIN);   // not 0: an unseen key stays at -inf
+          if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = fmaxf(sk1 * row.mul[j], FLT_MIN);
+        }
+        if (p.cap_in > 0.f || p.slopes) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float v = s[nb][mt][2 * u + j] * (mt ? f1 : f0);
-              const int tok = mt * 16 + 8 * u + g8, key = base + tok;
+            for (int k = 0; k < 4; ++k) {
+              float v = s[nb][mt][k] * f[nb][PT == 16 ? mt : 0][k & 1];
               if (p.cap_in > 0.f)   // softcap tanh(x / softcap) = softcap (1 - 2 / (1 + e^(2 x / softcap)))
                 v = fmaf(-2.f * p.cap_log2, rcp_fast(1.f + ex2(v * p.cap_in)), p.cap_log2);
-              if (p.slopes) v = fmaf(-slope[nb][j], fabsf((float)(key - pos[nb][j])), v);
-              if (!whole && (key < lo[nb][j] || key > hi[nb][j] || (gone >> tok & 1))) v = -INFINITY;
-              s[nb][mt][2 * u + j] = v;
-              mx[nb][j] = fmaxf(mx[nb][j], v);
+              if (p.slopes) {       // positions are below 2^24: exact in fp32
+                const float dist = (float)(base + g8 + mt * 16 + 8 * (k >> 1)) - row.pos[k & 1];
+                v = fmaf(-row.slope[k & 1], fabsf(dist), v);
+              }
+              s[nb][mt][k] = v;
             }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f[nb][0][j] = 1.f;
+            if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = 1.f;
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int tok = mt * 16 + 8 * u + g8;
+                if (base + tok < row.lo[j] || base + tok > row.hi[j] || (gone >> tok & 1)) s[nb][mt][2 * u + j] = -INFINITY;
+              }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float mx0 = fmaxf(s[nb][0][j], s[nb][0][2 + j]), mx1 = fmaxf(s[nb][1][j], s[nb][1][2 + j]);
+          if (PT == 16) mx[nb][j] = fmaxf(mx0 * f[nb][0][j], mx1 * f[nb][PT == 16 ? 1 : 0][j]);
+          else mx[nb][j] = fmaxf(mx0, mx1) * f[nb][0][j];
           grow |= mx[nb][j] > m[nb][j] + kLazyMax;
         }
       }
@@ -520,11 +648,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float m_new = fmaxf(m[nb][j], v);
-            const float f = m_new == -INFINITY ? 1.f : ex2(m[nb][j] - m_new);
+            const float r = m_new == -INFINITY ? 1.f : ex2(m[nb][j] - m_new);
             m[nb][j] = m_new;
-            l[nb][j] *= f;
+            l[nb][j] *= r;
 #pragma unroll
-            for (int dt = 0; dt < 8; ++dt) o[nb][dt][j] *= f, o[nb][dt][2 + j] *= f;
+            for (int dt = 0; dt < 8; ++dt) o[nb][dt][j] *= r, o[nb][dt][2 + j] *= r;
           }
       }
       uint32_t pf[NB][2][2];   // weights as B fragments
@@ -535,39 +663,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float a = ex2(s[nb][mt][2 * u] - ref0), c = ex2(s[nb][mt][2 * u + 1] - ref1);
+            const float* fm = f[nb][PT == 16 ? mt : 0];
+            const float a = ex2(fmaf(s[nb][mt][2 * u], fm[0], -ref0)), c = ex2(fmaf(s[nb][mt][2 * u + 1], fm[1], -ref1));
             l[nb][0] += a;
             l[nb][1] += c;
             pf[nb][mt][u] = movmatrix_t(cvt_f16x2(a, c));
           }
       }
+      // the sums of values' products start from minus what the shift adds to them
+      float t0[NB][PT == 16 ? 2 : 1][4];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          float(&t)[4] = t0[nb][PT == 16 ? mt : 0];
+          if (mt == 0 || PT == 16) t[0] = t[1] = t[2] = t[3] = 0.f;
+          if (kInt) mma_f16(t, minus_shift, pf[nb][mt][0], pf[nb][mt][1], t);
+        }
+
+      if (!wait_unit()) break;
+      unsigned char* vt = ring + slot * kUnitBytes;
+      const float sv0 = sh.scale[warp][slot][0], sv1 = PT == 16 ? sh.scale[warp][slot][1] : sv0;
+      if (!kInt && gone) {   // what lies there may be a NaN, which a zero weight keeps: clear those rows
+        if (gone >> lane & 1) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(vt + lane * kD + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      const uint32_t vrow = smem_u32(vt) + lane * kD + ((lane & 7) << 4);
 #pragma unroll
       for (int dt = 0; dt < 8; ++dt) {
         uint32_t r[4], a[2][4];
-        ldsm_x4_t(r[0], r[1], r[2], r[3], vt + lane * kD + ((dt ^ (lane & 7)) << 4));
+        ldsm_x4_t_at(r, vrow ^ (dt << 4));
         codes_evenodd<CODE>(r[0], a[0][0], a[0][1]);
         codes_evenodd<CODE>(r[1], a[0][2], a[0][3]);
         codes_evenodd<CODE>(r[2], a[1][0], a[1][1]);
         codes_evenodd<CODE>(r[3], a[1][2], a[1][3]);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          float t[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816_f16(t, a[0][0], a[0][1], a[0][2], a[0][3], pf[nb][0][0], pf[nb][0][1]);
+          float t[4];
+          mma_f16(t, a[0], pf[nb][0][0], pf[nb][0][1], t0[nb][0]);
           if (PT == 16) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[nb][dt][k] = fmaf(sv0, t[k], o[nb][dt][k]), t[k] = 0.f;
+            for (int k = 0; k < 4; ++k) o[nb][dt][k] = fmaf(sv0, t[k], o[nb][dt][k]);
+            mma_f16(t, a[1], pf[nb][1][0], pf[nb][1][1], t0[nb][PT == 16 ? 1 : 0]);
+          } else {
+            mma_f16(t, a[1], pf[nb][1][0], pf[nb][1][1], t);
           }
-          mma_16816_f16(t, a[1][0], a[1][1], a[1][2], a[1][3], pf[nb][1][0], pf[nb][1][1]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[nb][dt][k] = fmaf(sv1, t[k], o[nb][dt][k]);
         }
       }
-      ++used;
-      __syncwarp();   // the stage is free
-      if (prod.x < end) {
-        prod.issue(p, sh, per_thread, hr_n, ring, warp, lane, st);
-        ++issued;
-      }
+      next_unit();
     }
     x += n_tiles;
 #pragma unroll
@@ -578,7 +727,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
       }
-    if (at.tile == 0 && n_tiles == at.s.tiles) {   // the whole sequence: write it
+    if (at.tile == 0 && n_tiles == at.s.tiles) {   // the whole segment: write it
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -593,10 +742,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
                 l[nb][j] > 0.f ? cvt_bf16x2(o[nb][dt][j] * inv, o[nb][dt][2 + j] * inv) : 0u;
         }
     } else {
-      const int slot = x < end ? 0 : 1;
+      const int late = x < end ? 0 : 1;
       // the last piece goes into the ring (nothing is in flight any more), an early one into the workspace
-      float* rec = slot ? reinterpret_cast<float*>(ring)
-                        : p.recs + ((size_t)blockIdx.x * (2 + kAttnWarps) + 2 + warp) * kRec;
+      float* rec = late ? reinterpret_cast<float*>(ring) : p.recs + ((size_t)blockIdx.x * (2 + W) + 2 + warp) * kRec;
       __syncwarp();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -609,7 +757,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
           if (g8 == 0) rec[ROWS * kD + r] = m[nb][j], rec[ROWS * kD + ROWS + r] = l[nb][j];
         }
       if (lane == 0) {
-        Piece& pc = sh.piece[warp][slot];
+        Piece& pc = sh.piece[warp][late];
         pc.seg = at.seg;
         pc.b = at.b;
         pc.hr = at.hr;
@@ -622,60 +770,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   __syncthreads();
   if (sh.abort && tid == 0) atomicOr(p.C.dev_status, LRKV_DEV_WAIT_TIMEOUT);
 
-  // join the warps' pieces, sequence by sequence
-  bool shared_rec[2] = {false, false};
-  Piece shared_piece[2];
-  for (int i = 0; i < 2 * kAttnWarps;) {
-    const Piece first = sh.piece[i >> 1][i & 1];
-    if (first.seg < 0) {
-      ++i;
-      continue;
-    }
-    int idx[2 * kAttnWarps], n = 0;
-    for (; i < 2 * kAttnWarps; ++i) {
-      const long long seg = sh.piece[i >> 1][i & 1].seg;
-      if (seg < 0) continue;
-      if (seg != first.seg) break;
-      idx[n++] = i;
-    }
-    auto rec = [&](int k) -> const float* {
-      const int w = idx[k] >> 1;
-      return idx[k] & 1 ? reinterpret_cast<const float*>(sm + w * kWarpRing)
-                        : p.recs + ((size_t)blockIdx.x * (2 + kAttnWarps) + 2 + w) * kRec;
-    };
-    const int h = first.hr / p.row_blocks, rho0 = first.hr % p.row_blocks * p.per_block;
+  // query rows of a piece's sequence, and the first of its block
+  auto piece_rows = [&](const Piece& pc, int* rho0, int* h) {
     uint32_t st = 0;
-    const int rows_b = p.g * call_tokens(p.t_q_b, first.b, p.t_q, &st);
-    const int rho1 = min(min(rho0 + p.per_block, p.g * p.t_q), rows_b);
-    const bool done = first.seg >= X0 && first.seg + first.tiles <= X1;
-    const int which = first.seg >= X0 ? 1 : 0;
-    float* dst = p.recs + ((size_t)blockIdx.x * (2 + kAttnWarps) + which) * kRec;
-    for (int e = tid; e < ROWS * (kD / 4); e += kAttnThreads) {
-      const int row = e / (kD / 4), d = e % (kD / 4) * 4;
-      if (rho0 + row >= rho1) continue;
+    *h = pc.hr / p.row_blocks;
+    *rho0 = pc.hr % p.row_blocks * p.per_block;
+    return min(min(*rho0 + p.per_block, p.g * p.t_q), p.g * call_tokens(p.t_q_b, pc.b, p.t_q, &st));
+  };
+  // join the pieces of a segment: the warps that hold them share the rows
+  for (int k = 0; k < 2; ++k) {
+    const Piece mine = sh.piece[warp][k];
+    if (mine.seg < 0) continue;
+    const int seg = lane < 2 * W ? sh.piece[lane >> 1][lane & 1].seg : -1;
+    const uint32_t members = __ballot_sync(0xffffffffu, seg == mine.seg);
+    const int n = __popc(members), rank = __popc(members & ((1u << (2 * warp + k)) - 1u));
+    const int place = nth_bit(members, min(lane, n - 1)), w = place >> 1;
+    const float* rec = place & 1 ? reinterpret_cast<const float*>(sm + w * C::kWarpBytes)
+                                 : p.recs + ((size_t)blockIdx.x * (2 + W) + 2 + w) * kRec;
+    int rho0, h;
+    const int rho1 = piece_rows(mine, &rho0, &h);
+    const bool done = mine.seg >= X0 && mine.seg + mine.tiles <= X1;
+    const int which = mine.seg >= X0 ? 1 : 0;
+    float* dst = p.recs + ((size_t)blockIdx.x * (2 + W) + which) * kRec;
+    for (int row = rank; rho0 + row < rho1; row += n) {
       float4 o;
       float m, l;
-      join_rows(n, rec, ROWS, row, d, o, m, l);
+      join_row(n, rec, ROWS, row, lane, o, m, l);
       if (done) {
-        store_row4(p.out + row_offset(p, first.b, h, rho0 + row) + d, o, l);
+        store_row4(p.out + row_offset(p, mine.b, h, rho0 + row) + 4 * lane, o, l);
       } else {
-        *reinterpret_cast<float4*>(dst + row * kD + d) = o;
-        if (d == 0) dst[ROWS * kD + row] = m, dst[ROWS * kD + ROWS + row] = l;
+        *reinterpret_cast<float4*>(dst + row * kD + 4 * lane) = o;
+        if (lane == 0) dst[ROWS * kD + row] = m, dst[ROWS * kD + ROWS + row] = l;
       }
     }
-    if (!done) {
-      if (which) shared_rec[1] = true, shared_piece[1] = first;
-      else shared_rec[0] = true, shared_piece[0] = first;
-    }
+    if (!done && rank == 0 && lane == 0) sh.open[which] = mine;
   }
-  if (!shared_rec[0] && !shared_rec[1]) return;
   __syncthreads();
-  auto cta_of = [&](long long tile) { return (int)(((tile + 1) * ctas + T - 1) / T - 1); };
+  Piece shared_piece[2] = {sh.open[0], sh.open[1]};
+  if (shared_piece[0].seg < 0 && shared_piece[1].seg < 0) return;
+  auto cta_of = [&](int tile) { return workers.of(tile) / W; };
   if (tid == 0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       sh.last[k] = 0;
-      if (!shared_rec[k]) continue;
+      if (shared_piece[k].seg < 0) continue;
       const int c0 = cta_of(shared_piece[k].seg), c1 = cta_of(shared_piece[k].seg + shared_piece[k].tiles - 1);
       if (atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0) {
         p.tickets[c0] = 0;
@@ -686,23 +824,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (!shared_rec[k] || !sh.last[k]) continue;
+    if (shared_piece[k].seg < 0 || !sh.last[k]) continue;
     const Piece first = shared_piece[k];
     const int c0 = cta_of(first.seg), c1 = cta_of(first.seg + first.tiles - 1);
-    auto rec = [&](int i) -> const float* {
-      return p.recs + ((size_t)(c0 + i) * (2 + kAttnWarps) + (i == 0 ? 1 : 0)) * kRec;
-    };
-    const int h = first.hr / p.row_blocks, rho0 = first.hr % p.row_blocks * p.per_block;
-    uint32_t st = 0;
-    const int rows_b = p.g * call_tokens(p.t_q_b, first.b, p.t_q, &st);
-    const int rho1 = min(min(rho0 + p.per_block, p.g * p.t_q), rows_b);
-    for (int e = tid; e < ROWS * (kD / 4); e += kAttnThreads) {
-      const int row = e / (kD / 4), d = e % (kD / 4) * 4;
-      if (rho0 + row >= rho1) continue;
-      float4 o;
-      float m, l;
-      join_rows(c1 - c0 + 1, rec, ROWS, row, d, o, m, l);
-      store_row4(p.out + row_offset(p, first.b, h, rho0 + row) + d, o, l);
+    int rho0, h;
+    const int rho1 = piece_rows(first, &rho0, &h);
+    const int n = c1 - c0 + 1;
+    for (int row = warp; rho0 + row < rho1; row += W) {
+      // up to 32 records at a time
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float m = -INFINITY, l = 0.f;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float4 o1;
+        float m1, l1;
+        const int i = min(i0 + lane, n - 1);
+        const float* rec = p.recs + ((size_t)(c0 + i) * (2 + W) + (i == 0 ? 1 : 0)) * kRec;
+        join_row(min(32, n - i0), rec, ROWS, row, lane, o1, m1, l1);
+        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm, w = ex2(m - ref), w1 = ex2(m1 - ref);
+        o = make_float4(o.x * w + o1.x * w1, o.y * w + o1.y * w1, o.z * w + o1.z * w1, o.w * w + o1.w * w1);
+        l = l * w + l1 * w1;
+        m = mm;
+      }
+      store_row4(p.out + row_offset(p, first.b, h, rho0 + row) + 4 * lane, o, l);
     }
   }
 }

@@ -6,7 +6,7 @@ and types; the same names as in the C ABI are re-exported by the package.
 """
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -74,8 +74,20 @@ def load_serve_library(path=None):
     return lib
 
 
+class _Fields:
+    """Copies and pickles take a dataclass's fields; what __post_init__ derives from them is made anew."""
+
+    def __getstate__(self):
+        return {f.name: getattr(self, f.name) for f in fields(self)}
+
+    def __setstate__(self, state):
+        for name, value in state.items():
+            object.__setattr__(self, name, value)
+        self.__post_init__()
+
+
 @dataclass(frozen=True)
-class Score:
+class Score(_Fields):
     """Score modifiers (``lrkv_score``): scale 0 stands for 1/sqrt(d), softcap and
     window 0 for none; slopes [Hq] fp32; first_key and prefix_end [B, t_q] int32."""
     scale: float = 0.0
@@ -85,13 +97,17 @@ class Score:
     first_key: torch.Tensor = None
     prefix_end: torch.Tensor = None
 
+    def __post_init__(self):
+        plain = self.slopes is None and self.first_key is None and self.prefix_end is None
+        object.__setattr__(self, "_plain", ctypes.byref(self.c()) if plain else None)
+
     def c(self):
         return _Score(self.scale, self.softcap, self.window, _addr(self.slopes), _addr(self.first_key),
                       _addr(self.prefix_end))
 
 
 @dataclass(frozen=True)
-class PagedDims:
+class PagedDims(_Fields):
     B: int
     Hq: int
     Hkv: int
@@ -101,6 +117,9 @@ class PagedDims:
     max_pages: int
     n_layers: int = 1
     code: str = "int8"
+
+    def __post_init__(self):
+        object.__setattr__(self, "_ref", ctypes.byref(self.c()))
 
     def c(self):
         return _PagedDims(self.B, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages, self.n_layers,
@@ -138,7 +157,9 @@ class PagedCache:
         self.dims = dims
 
     def c(self):
-        return _PagedCache(*[getattr(self, f).data_ptr() for f in self.FIELDS])
+        return _PagedCache(self.k.data_ptr(), self.v.data_ptr(), self.scale_k.data_ptr(), self.scale_v.data_ptr(),
+                           self.page_table.data_ptr(), self.seq_len.data_ptr(), self.refs.data_ptr(),
+                           self.dev_status.data_ptr())
 
     def nbytes(self):
         return sum(getattr(self, f).numel() * getattr(self, f).element_size() for f in self.FIELDS)
@@ -149,32 +170,59 @@ def _addr(t):
 
 
 def _check(t, name, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}" + ("" if t.is_contiguous() else ", not contiguous"))
 
 
 def _check_score(score, B, t_q, Hq):
-    if score is None:
+    if score is None or score._plain is not None:
         return
     for name, shape, dtype in (("slopes", (Hq,), torch.float32), ("first_key", (B, t_q), torch.int32),
                                ("prefix_end", (B, t_q), torch.int32)):
         t = getattr(score, name)
         if t is not None:
             _check(t, name, shape, dtype)
+            _same_device(t, name)
 
 
 def _check_list(t, name, n):
     if t is not None:
         _check(t, name, (n,), torch.int32)
+        _same_device(t, name)
+
+
+def _same_device(t, name):
+    # the library launches on the current device, whatever device the tensors are on
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {t.device}")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _check_ws(ws):
+    if ws is not None:
+        if ws.dtype != torch.uint8 or not ws.is_contiguous():
+            raise ValueError("ws: a contiguous uint8 tensor is needed")
+        _same_device(ws, "ws")
 
 
 def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    # current_stream() builds an object (3 us); the raw handle is what the library takes
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def _ref(score):
-    return None if score is None else ctypes.byref(score.c())
+    if score is None:
+        return None
+    return score._plain if score._plain is not None else ctypes.byref(score.c())
+
+
+def _cache_ref(dims, cache):
+    if cache.dims is not dims and cache.dims != dims:
+        raise ValueError(f"the cache was made for {cache.dims}, not {dims}")
+    _same_device(cache.k, "cache")
+    return ctypes.byref(cache.c())
 
 
 def _done(code, what, check):
@@ -184,13 +232,24 @@ def _done(code, what, check):
     return code
 
 
+_Int64x3 = ctypes.c_int64 * 3
+
+
 def _strides(t):
-    return (ctypes.c_int64 * 3)(*t.stride()[:3])
+    a, b, c, _ = t.stride()
+    return _Int64x3(a, b, c)
 
 
 def _prefill_dims(q, k, v, out):
     B, t_q, Hq, d = q.shape
-    return _PrefillDims(B, Hq, k.shape[2], d, t_q, k.shape[1], _strides(q), _strides(k), _strides(v), _strides(out))
+    _, t_k, Hkv, _ = k.shape
+    return _PrefillDims(B, Hq, Hkv, d, t_q, t_k, _strides(q), _strides(k), _strides(v), _strides(out))
+
+
+def _check_rows(t, name):
+    if t.dtype != torch.bfloat16 or t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
+        raise ValueError(f"{name}: a bf16 tensor [B, t, heads, d] with contiguous rows is needed")
+    _same_device(t, name)
 
 
 def lrkv_prefill_workspace_size(q, k, v, out):
@@ -202,27 +261,32 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
     """out [B,t_q,Hq,d] <- attention of q [B,t_q,Hq,d] over k, v [B,t_k,Hkv,d] (bf16, rows of d contiguous
     elements, otherwise any strides); see include/lrkv_serve.h.  A workspace is made when one is needed
     and none is given."""
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-            raise ValueError(f"{name}: a bf16 tensor [B, t, heads, d] with contiguous rows is needed")
+    _check_rows(q, "q")
+    _check_rows(k, "k")
+    _check_rows(v, "v")
+    _check_rows(out, "out")
     B, t_q, Hq, d = q.shape
-    if tuple(out.shape) != tuple(q.shape) or tuple(k.shape) != tuple(v.shape) or k.shape[0] != B or k.shape[3] != d:
+    if out.shape != q.shape or k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
         raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
                          f"out {tuple(out.shape)}")
     _check_list(q_len, "q_len", B)
     _check_list(kv_len, "kv_len", B)
     _check_score(score, B, t_q, Hq)
-    lib, dims = load_serve_library(), _prefill_dims(q, k, v, out)
-    need = lib.lrkv_prefill_workspace_size(ctypes.byref(dims))
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    return _done(lib.lrkv_prefill_attn(ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_len),
-                                       _addr(kv_len), _ref(score), out.data_ptr(), _addr(dev_status), _addr(ws),
+    if dev_status is not None:
+        _same_device(dev_status, "dev_status")
+    _check_ws(ws)
+    lib, dims = load_serve_library(), ctypes.byref(_prefill_dims(q, k, v, out))
+    if ws is None:
+        need = lib.lrkv_prefill_workspace_size(dims)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return _done(lib.lrkv_prefill_attn(dims, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_len), _addr(kv_len),
+                                       _ref(score), out.data_ptr(), _addr(dev_status), _addr(ws),
                                        0 if ws is None else ws.numel(), _stream(stream)), "lrkv_prefill_attn", check)
 
 
 def lrkv_paged_workspace_size(dims, t_q=1):
-    return int(load_serve_library().lrkv_paged_workspace_size(ctypes.byref(dims.c()), int(t_q)))
+    return int(load_serve_library().lrkv_paged_workspace_size(dims._ref, int(t_q)))
 
 
 def make_paged_workspace(dims, t_q=1, device="cuda"):
@@ -238,9 +302,10 @@ def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=Non
     t_new = k_new.shape[1]
     for name, t in (("k_new", k_new), ("v_new", v_new)):
         _check(t, name, (dims.B, t_new, dims.Hkv, dims.d), torch.bfloat16)
+        _same_device(t, name)
     _check_list(t_new_b, "t_new_b", dims.B)
     return _done(load_serve_library().lrkv_paged_append(
-        ctypes.byref(dims.c()), ctypes.byref(cache.c()), layer, k_new.data_ptr(), v_new.data_ptr(), t_new,
+        dims._ref, _cache_ref(dims, cache), layer, k_new.data_ptr(), v_new.data_ptr(), t_new,
         _addr(t_new_b), _stream(stream)), "lrkv_paged_append", check)
 
 
@@ -249,10 +314,11 @@ def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None,
     t_max = k_out.shape[1]
     for name, t in (("k_out", k_out), ("v_out", v_out)):
         _check(t, name, (dims.B, t_max, dims.Hkv, dims.d), torch.bfloat16)
+        _same_device(t, name)
     _check_list(first, "first", dims.B)
     _check_list(count, "count", dims.B)
     return _done(load_serve_library().lrkv_paged_read(
-        ctypes.byref(dims.c()), ctypes.byref(cache.c()), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
+        dims._ref, _cache_ref(dims, cache), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
         v_out.data_ptr(), _stream(stream)), "lrkv_paged_read", check)
 
 
@@ -261,24 +327,26 @@ def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None,
     t_q = q.shape[1]
     for name, t in (("q", q), ("out", out)):
         _check(t, name, (dims.B, t_q, dims.Hq, dims.d), torch.bfloat16)
+        _same_device(t, name)
     _check_list(t_q_b, "t_q_b", dims.B)
     _check_score(score, dims.B, t_q, dims.Hq)
+    _check_ws(ws)
     return _done(load_serve_library().lrkv_paged_attn(
-        ctypes.byref(dims.c()), ctypes.byref(cache.c()), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score),
+        dims._ref, _cache_ref(dims, cache), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score),
         out.data_ptr(), _addr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "lrkv_paged_attn", check)
 
 
 def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """Pages for t_new (or t_new_b[b]) more tokens of every sequence."""
     _check_list(t_new_b, "t_new_b", dims.B)
-    return _done(load_serve_library().lrkv_pages_reserve(ctypes.byref(dims.c()), ctypes.byref(cache.c()), t_new,
+    return _done(load_serve_library().lrkv_pages_reserve(dims._ref, _cache_ref(dims, cache), t_new,
                                                          _addr(t_new_b), _stream(stream)), "lrkv_pages_reserve", check)
 
 
 def lrkv_pages_advance(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """seq_len += t_new (or t_new_b)."""
     _check_list(t_new_b, "t_new_b", dims.B)
-    return _done(load_serve_library().lrkv_pages_advance(ctypes.byref(dims.c()), ctypes.byref(cache.c()), t_new,
+    return _done(load_serve_library().lrkv_pages_advance(dims._ref, _cache_ref(dims, cache), t_new,
                                                          _addr(t_new_b), _stream(stream)), "lrkv_pages_advance", check)
 
 
@@ -291,15 +359,16 @@ def _pair(src, dst):
 def lrkv_pages_fork(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Sequence dst[i] becomes a copy of sequence src[i] (int32 lists on the device)."""
     s, d, n = _pair(src, dst)
+    _check_ws(ws)
     return _done(load_serve_library().lrkv_pages_fork(
-        ctypes.byref(dims.c()), ctypes.byref(cache.c()), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
+        dims._ref, _cache_ref(dims, cache), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
         _stream(stream)), "lrkv_pages_fork", check)
 
 
 def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
     """Empty the sequences listed in seqs (int32, on the device)."""
     _check_list(seqs, "seqs", seqs.numel())
-    return _done(load_serve_library().lrkv_pages_free(ctypes.byref(dims.c()), ctypes.byref(cache.c()),
+    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache),
                                                       seqs.data_ptr(), seqs.numel(), _stream(stream)),
                  "lrkv_pages_free", check)
 
@@ -307,13 +376,15 @@ def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
 def lrkv_pages_copy(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Copy pages src[i] to dst[i] (int32 lists on the device) in every layer."""
     s, d, n = _pair(src, dst)
+    _check_ws(ws)
     return _done(load_serve_library().lrkv_pages_copy(
-        ctypes.byref(dims.c()), ctypes.byref(cache.c()), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
+        dims._ref, _cache_ref(dims, cache), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
         _stream(stream)), "lrkv_pages_copy", check)
 
 
 def lrkv_pages_compact(dims, cache, ws=None, stream=None, check=True):
     """Move pages so that the live ones have the lowest ids."""
-    return _done(load_serve_library().lrkv_pages_compact(ctypes.byref(dims.c()), ctypes.byref(cache.c()), _addr(ws),
+    _check_ws(ws)
+    return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache), _addr(ws),
                                                          0 if ws is None else ws.numel(), _stream(stream)),
                  "lrkv_pages_compact", check)

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(sm + kOffBar);
   volatile int* abort_flag = &bars->abort;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // the last query blocks first: under a causal mask they are the longest
   const int hb = blockIdx.x % (p.Hq * p.B);
@@ -169,14 +169,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc5::fence_before_sync();
   __syncthreads();
   tc5::fence_after_sync();
-  const uint32_t tmem = bars->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
   // tiles [t0[x], t1[x]) of block x; [j0, j1) of the CTA
   int t0[2], t1[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const bool any = bars->hi[x] >= 0;
-    t0[x] = any ? bars->lo[x] / kTile : 0x7fffffff;
-    t1[x] = any ? bars->hi[x] / kTile + 1 : 0;
+    t0[x] = __shfl_sync(0xffffffffu, any ? bars->lo[x] / kTile : 0x7fffffff, 0);   // known to be uniform
+    t1[x] = __shfl_sync(0xffffffffu, any ? bars->hi[x] / kTile + 1 : 0, 0);
   }
   const int j0 = min(t0[0], t0[1]), j1 = max(t1[0], t1[1]);
 
@@ -221,26 +221,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (j0 < j1) {
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kTile, kTile);
       constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kTile, kD);
-      const uint32_t qb = smem_u32(sm + kOffQ), kb = smem_u32(sm + kOffK), vb = smem_u32(sm + kOffV);
+      // descriptors of the first operands; an offset in shared memory adds its sixteenths
+      const uint64_t dq = tc5::smem_desc(smem_u32(sm + kOffQ), 16, 1024, tc5::kSwizzle128B);
+      const uint64_t dk = tc5::smem_desc(smem_u32(sm + kOffK), 16, 1024, tc5::kSwizzle128B);
+      const uint64_t dv = tc5::smem_desc(smem_u32(sm + kOffV), kBoxBytes, 1024, tc5::kSwizzle128B);
       auto issue_s = [&](int x, int j) {   // S_x = Q_x K_j^T
-        if (lane == 0) {
-          const uint32_t ks = kb + ((j - j0) % kKStages) * kTileBytes, qs = qb + x * kTileBytes;
+        if (elect_one()) {
+          const uint64_t ks = dk + ((j - j0) % kKStages) * (kTileBytes >> 4), qs = dq + x * (kTileBytes >> 4);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint32_t off = (c >> 2) * kBoxBytes + (c & 3) * 32;
-            tc5::mma_bf16(tmem + kColS + 128 * x, tc5::smem_desc(qs + off, 16, 1024, tc5::kSwizzle128B),
-                          tc5::smem_desc(ks + off, 16, 1024, tc5::kSwizzle128B), idesc_s, c > 0);
+            const uint32_t off = ((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4;
+            tc5::mma_bf16(tmem + kColS + 128 * x, qs + off, ks + off, idesc_s, c > 0);
           }
           tc5::mma_commit(&bars->s_full[x]);
         }
       };
       auto issue_o = [&](int x, int j) {   // O_x += P_x V_j
-        if (lane == 0) {
-          const uint32_t vs = vb + ((j - j0) % kVStages) * kTileBytes;
+        if (elect_one()) {
+          const uint64_t vs = dv + ((j - j0) % kVStages) * (kTileBytes >> 4);
 #pragma unroll
           for (int c = 0; c < 8; ++c)      // 16 keys: two 8-row groups of both 64-column boxes
-            mma_bf16_ta(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * c,
-                        tc5::smem_desc(vs + c * 2048, kBoxBytes, 1024, tc5::kSwizzle128B), idesc_o,
+            mma_bf16_ta(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * c, vs + c * (2048 >> 4), idesc_o,
                         j > t0[x] || c > 0);
           if (j == t1[x] - 1) tc5::mma_commit(&bars->o_full[x]);
         }
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tc5::fence_after_sync();
         for (int x = 0; x < 2; ++x)
           if (t0[x] == j0) issue_s(x, j0);
-        if (lane == 0) tc5::mma_commit(&bars->k_empty[0]);
+        if (elect_one()) tc5::mma_commit(&bars->k_empty[0]);
       }
       int done[2] = {0, 0};   // P tiles taken per block
       for (int j = j0; ok && j < j1; ++j) {
@@ -284,16 +285,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (more && j + 1 >= t0[x] && j + 1 < t1[x]) issue_s(x, j + 1);
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc5::mma_commit(&bars->v_empty[vi % kVStages]);
           if (more) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
         }
       }
       // every MMA done before tensor memory is freed
-      if (lane == 0) {
-        tc5::mma_commit(&bars->drain);
-        mbar_wait_bounded(&bars->drain, 0, kWaitIters);
-      }
+      __syncwarp();
+      if (elect_one()) tc5::mma_commit(&bars->drain);
+      mbar_wait_bounded(&bars->drain, 0, kWaitIters);
       __syncwarp();
     }
   } else {

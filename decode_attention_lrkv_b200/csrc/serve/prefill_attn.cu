@@ -10,7 +10,7 @@ namespace {
 using namespace lrkv;
 
 // Rows [B][t][H][128] as a 4-d tensor (128, H, t, B): boxes of 64 columns x 1 head
-// x 128 tokens, 128-byte swizzle, zeros past the last token of a batch row.
+// x 64 tokens, 128-byte swizzle, zeros past the last token of a batch row.
 bool rows_map(CUtensorMap* map, const lrkv_bf16* base, int B, int t, int H, const int64_t (&st)[3]) {
   serve::EncodeTiledFn enc = serve::encode_tiled();
   if (!enc) return false;
@@ -20,7 +20,7 @@ bool rows_map(CUtensorMap* map, const lrkv_bf16* base, int B, int t, int H, cons
   const cuuint64_t stt = t > 1 ? (cuuint64_t)st[1] * 2 : (cuuint64_t)kD * 2;
   const cuuint64_t sb = B > 1 ? (cuuint64_t)st[0] * 2 : (cuuint64_t)kD * 2;
   const cuuint64_t strides[3] = {sh, stt, sb};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)prefill::kTile, 1};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)prefill::kUnit, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<lrkv_bf16*>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -100,6 +100,9 @@ lrkv_status lrkv_prefill_attn(const lrkv_prefill_dims* dims, const lrkv_bf16* q,
   p.qk_log2 = sc.scale * kLog2e;
   const bool cap = sc.softcap > 0.f, bias = sc.slopes != nullptr;
   if (cap) {
+    constexpr float kTanh[6] = {0.9999994f, -0.33329043f, 0.13281433f, -0.051605646f, 0.016743084f, -0.0030670483f};
+    for (int i = 0; i < 6; ++i) p.cap_poly[i] = sc.softcap * kLog2e * kTanh[i];
+    p.cap_unit = sc.scale / sc.softcap;
     p.cap_in = 2.f * kLog2e * sc.scale / sc.softcap;
     p.cap_log2 = sc.softcap * kLog2e;
   }

@@ -2,31 +2,37 @@
 //
 // For every query row i of a head:  o_i = sum_j p_ij v_j / sum_j p_ij,
 // p_ij = exp(s_ij - m_i), s_ij the modified scores (lrkv_score), m_i a running
-// reference close to the row's maximum; one pass over the keys in tiles of 128.
+// reference close to the row's maximum; one pass over the keys in units of 64.
 //
-// A CTA takes two blocks of 128 query rows (X = 0, 1) of one head.  Per key tile
-// and block:
-//     S_X = Q_X K^T      (M 128, N 128, K 128; operands in shared memory)
+// A CTA takes two blocks of 128 query rows (X = 0, 1) of one head.  Per unit and block:
+//     S_X = Q_X K^T      (M 128, N 64, K 128; operands in shared memory)
 //     P_X = exp2(S_X ..) (a thread per row; P_X overwrites S_X as packed bf16)
-//     O_X += P_X V       (M 128, N 128, K 128; P_X read from tensor memory)
-// S_0, S_1, O_0, O_1 fill the 512 columns of tensor memory.  One warp issues TMA
-// loads (128-byte swizzle, rings of key and value tiles), one issues MMAs, two
-// groups of four warps do the softmax of a block each.  The MMA warp alternates
-// between the blocks, so the tensor cores work on one block while the other's
-// softmax runs.
+//     O_X += P_X V       (M 128, N 128, K 64; P_X read from tensor memory)
+// A block's scores have two places of 64 columns, for even and odd units: with
+// O_0, O_1 they fill the 512 columns of tensor memory.  One warp issues TMA loads
+// (128-byte swizzle, rings of key and value units), two issue the MMAs of a block
+// each, two groups of four warps do the softmax of a block each.  When a block's P of
+// unit u arrives its MMA warp issues O += P V of u and S of unit u + 2, so the group
+// finds the scores of u + 1 ready: the tensor cores run beside the softmax of the same
+// block, not only of the other one.  (One MMA warp for both blocks: 689 us where 511
+// had been with units of 128 keys; it spent 1200 clocks a unit on its four waits.)
 //
-// Bound: a tile pair costs 2 x 2 x 2 x 128^3 tensor flops and 2 x 128^2
-// exponentials; at 8192 flops and 16 exponentials a clock and SM both take 2048
-// clocks, so the softmax's instruction count decides.
+// Bound: a unit of both blocks costs 2 x 2 x 2 x 128 x 64 x 128 tensor flops and
+// 2 x 128 x 64 exponentials; at 8192 flops and 16 exponentials a clock and SM both take
+// 1024 clocks (1148 measured for the products: S with N = 64 reads shared memory at
+// 48 clocks per step where 32 would do), so the softmax's instruction count decides:
+// two-wide fp32 instructions, three-input maxima.  With units of 128 keys (S and P in
+// the same columns, so S of the next unit waited for O += P V of this one) 8192 causal
+// tokens x 32 heads took 511 us.
 //
 // The running reference m only moves when a row's maximum passes it by more than
 // 2^8 (weights then stay below 2^8, and the row's sum is in fp32): O is rescaled
-// in tensor memory a few times per row instead of once per tile.  A softmax group
-// may touch O_X right after it sees S_X complete: MMAs complete in order, and the
-// next product into O_X waits for this group's P_X.
+// in tensor memory a few times per row instead of once per unit.  The group that does
+// it first waits for the scores of the next unit: MMAs complete in order, so the last
+// product into O is complete, and the next one waits for this group's P.
 //
-// Every mask is an interval [lo, hi] of keys per row, so a block's tiles are the
-// union of its rows' intervals, and a tile inside all of a warp's intervals is not
+// Every mask is an interval [lo, hi] of keys per row, so a block's units are the
+// union of its rows' intervals, and a unit inside all of a warp's intervals is not
 // masked at all.
 #pragma once
 
@@ -42,25 +48,28 @@ namespace prefill {
 
 using namespace serve;
 
-constexpr int kTile = 128;                  // query rows per block, keys per tile
-constexpr int kThreads = 320;               // warps 0-3, 4-7 softmax of block 0, 1; 8 TMA; 9 MMA
+constexpr int kTile = 128;                  // query rows per block
+constexpr int kUnit = 64;                   // keys per unit
+constexpr int kThreads = 352;               // warps 0-3, 4-7 softmax of block 0, 1; 8 TMA; 9, 10 MMA of block 0, 1
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kTileBytes = kTile * kD * 2;  // two boxes of 64 columns
 constexpr int kBoxBytes = kTileBytes / 2;
-constexpr int kKStages = 2, kVStages = 2;
+constexpr int kUnitBytes = kUnit * kD * 2;  // two boxes of 64 columns
+constexpr int kUnitBox = kUnitBytes / 2;
+constexpr int kKStages = 4, kVStages = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;  // + 128 X
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 X (+ 64 (unit & 1) for S)
 constexpr float kLazy = 8.f;                // rescale when a maximum grows by more (log2)
 
 // Shared memory: Q blocks, key ring, value ring (each 1024-aligned), barriers.
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
-constexpr int kOffV = kOffK + kKStages * kTileBytes;
-constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+constexpr int kOffV = kOffK + kKStages * kUnitBytes;
+constexpr int kOffBar = kOffV + kVStages * kUnitBytes;
 constexpr size_t kSmemBytes = kOffBar + 256 + 1024;
 
 struct Params {
-  CUtensorMap map_q, map_k, map_v;   // [B][t][H][128] as (128, H, t, B), box {64, 1, 128, 1}
+  CUtensorMap map_q, map_k, map_v;   // [B][t][H][128] as (128, H, t, B), box {64, 1, 64, 1}
   lrkv_bf16* out;
   int64_t os_b, os_t, os_h;
   const int32_t* q_len;
@@ -72,8 +81,10 @@ struct Params {
   int B, Hq, Hkv, t_q, t_k, window;
   int n_blocks;       // pairs of query blocks per (b, head)
   float qk_log2;      // scale * log2(e)
+  float cap_unit;     // scale / softcap
   float cap_in;       // 2 log2(e) scale / softcap
   float cap_log2;     // softcap * log2(e)
+  float cap_poly[6];  // softcap log2(e) tanh(x) = x (cap_poly[0] + cap_poly[1] x^2 + ..), |x| <= 1
   int out32;          // 32-byte stores allowed
 };
 
@@ -81,13 +92,47 @@ struct Bars {
   uint64_t q_full;
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2][2], p_full[2][2];   // [block][unit & 1]
   uint64_t drain;
   uint32_t tmem;
   int abort;
   int lo[2], hi[2];    // union of the rows' key intervals, per block
 };
 static_assert(sizeof(Bars) <= 256, "barrier region");
+
+// s[c] = softcap log2(e) tanh(scale s[c] / softcap).  Where all |x| = |scale s / softcap| of
+// the warp are at most 1, as sane logits are, by a polynomial in x^2 on the two-wide fp32
+// pipe (a least-squares fit of tanh(x) / x, weighted towards equal relative errors: 6.5e-7
+// at most with fp32 rounding, 4e-5 in the exponent at softcap 50); else by
+// tanh(x) = 1 - 2 / (1 + e^(2x)), two special-function results for each score.
+__device__ __forceinline__ void cap_scores(const Params& p, float (&s)[kUnit]) {
+  float top0 = 0.f, top1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < kUnit; c += 4) {
+    top0 = max3(top0, fabsf(s[c]), fabsf(s[c + 1]));
+    top1 = max3(top1, fabsf(s[c + 2]), fabsf(s[c + 3]));
+  }
+  // scores of keys past the sequence may be NaN, which a maximum drops; they are masked later
+  if (__all_sync(0xffffffffu, fmaxf(top0, top1) * p.cap_unit <= 1.f)) {
+    const f32x2 u = pack2(p.cap_unit, p.cap_unit);
+    f32x2 k[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) k[i] = pack2(p.cap_poly[i], p.cap_poly[i]);
+#pragma unroll
+    for (int c = 0; c < kUnit; c += 2) {
+      const f32x2 x = mul2(pack2(s[c], s[c + 1]), u), t = mul2(x, x);
+      f32x2 r = fma2(k[5], t, k[4]);
+      r = fma2(r, t, k[3]);
+      r = fma2(r, t, k[2]);
+      r = fma2(r, t, k[1]);
+      r = fma2(r, t, k[0]);
+      unpack2(mul2(x, r), s[c], s[c + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kUnit; ++c) s[c] = fmaf(-2.f * p.cap_log2, rcp_fast(1.f + ex2(s[c] * p.cap_in)), p.cap_log2);
+  }
+}
 
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
@@ -119,16 +164,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
-    for (int s = 0; s < kKStages; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 1);
-    for (int s = 0; s < kVStages; ++s) mbar_init(&bars->v_full[s], 1), mbar_init(&bars->v_empty[s], 1);
+    for (int s = 0; s < kKStages; ++s) mbar_init(&bars->k_full[s], 1), mbar_init(&bars->k_empty[s], 2);
+    for (int s = 0; s < kVStages; ++s) mbar_init(&bars->v_full[s], 1), mbar_init(&bars->v_empty[s], 2);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], kTile);
-      mbar_init(&bars->o_full[x], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&bars->s_full[x][i], 1), mbar_init(&bars->p_full[x][i], kTile);
       bars->lo[x] = 0x7fffffff;
       bars->hi[x] = -1;
     }
-    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->drain, 2);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -170,13 +213,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc5::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem, 0);
-  // tiles [t0[x], t1[x]) of block x; [j0, j1) of the CTA
+  // units [t0[x], t1[x]) of block x; [j0, j1) of the CTA
   int t0[2], t1[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const bool any = bars->hi[x] >= 0;
-    t0[x] = __shfl_sync(0xffffffffu, any ? bars->lo[x] / kTile : 0x7fffffff, 0);   // known to be uniform
-    t1[x] = __shfl_sync(0xffffffffu, any ? bars->hi[x] / kTile + 1 : 0, 0);
+    t0[x] = __shfl_sync(0xffffffffu, any ? bars->lo[x] / kUnit : 0x7ffffff0, 0);   // known to be uniform
+    t1[x] = __shfl_sync(0xffffffffu, any ? bars->hi[x] / kUnit + 1 : 0, 0);
   }
   const int j0 = min(t0[0], t0[1]), j1 = max(t1[0], t1[1]);
 
@@ -187,26 +230,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          tma_load_4d(sm + kOffQ + x * kTileBytes + c * kBoxBytes, &p.map_q, 64 * c, h, row0 + x * kTile, b,
-                      &bars->q_full);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            tma_load_4d(sm + kOffQ + x * kTileBytes + c * kBoxBytes + r * kUnitBox, &p.map_q, 64 * c, h,
+                        row0 + x * kTile + r * kUnit, b, &bars->q_full);
       auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, int off, int ns, int j) {
         const int i = j - j0, s = i % ns;
         if (i >= ns && !wait_or_abort(&empty[s], ((i / ns) - 1) & 1, abort_flag)) return false;
-        mbar_arrive_expect_tx(&full[s], kTileBytes);
-        unsigned char* dst = sm + off + s * kTileBytes;
-        tma_load_4d(dst, map, 0, hk, j * kTile, b, &full[s]);
-        tma_load_4d(dst + kBoxBytes, map, 64, hk, j * kTile, b, &full[s]);
+        mbar_arrive_expect_tx(&full[s], kUnitBytes);
+        unsigned char* dst = sm + off + s * kUnitBytes;
+        tma_load_4d(dst, map, 0, hk, j * kUnit, b, &full[s]);
+        tma_load_4d(dst + kUnitBox, map, 64, hk, j * kUnit, b, &full[s]);
         return true;
       };
-      int nk = 0, nv = 0;   // tiles loaded
-      bool ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j0);
-      if (ok) ++nk;
-      for (int j = j0; ok && j < j1; ++j) {
-        if (j + 1 < j1) {
-          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 1);
+      int nk = 0, nv = 0;   // units loaded
+      bool ok = true;
+      for (int j = j0 - 2; ok && j < j1; ++j) {
+        if (j + 2 < j1) {
+          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 2);
           if (!ok) break;
           ++nk;
         }
+        if (j < j0) continue;
         ok = load(&p.map_v, bars->v_full, bars->v_empty, kOffV, kVStages, j);
         if (ok) ++nv;
       }
@@ -217,78 +262,64 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int i = nv > kVStages ? nv - kVStages : 0; i < nv; ++i)
         mbar_wait_bounded(&bars->v_full[i % kVStages], (i / kVStages) & 1, kWaitIters);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     if (j0 < j1) {
-      constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kTile, kTile);
+      const int x = warp - kMmaWarp, first = x ? t0[1] : t0[0], end = x ? t1[1] : t1[0];
+      constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kTile, kUnit);
       constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kTile, kD);
+      const uint32_t ts = tmem + kColS + 128 * x, to = tmem + kColO + 128 * x;
       // descriptors of the first operands; an offset in shared memory adds its sixteenths
-      const uint64_t dq = tc5::smem_desc(smem_u32(sm + kOffQ), 16, 1024, tc5::kSwizzle128B);
+      const uint64_t dq = tc5::smem_desc(smem_u32(sm + kOffQ + x * kTileBytes), 16, 1024, tc5::kSwizzle128B);
       const uint64_t dk = tc5::smem_desc(smem_u32(sm + kOffK), 16, 1024, tc5::kSwizzle128B);
-      const uint64_t dv = tc5::smem_desc(smem_u32(sm + kOffV), kBoxBytes, 1024, tc5::kSwizzle128B);
-      auto issue_s = [&](int x, int j) {   // S_x = Q_x K_j^T
-        if (elect_one()) {
-          const uint64_t ks = dk + ((j - j0) % kKStages) * (kTileBytes >> 4), qs = dq + x * (kTileBytes >> 4);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint32_t off = ((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4;
-            tc5::mma_bf16(tmem + kColS + 128 * x, qs + off, ks + off, idesc_s, c > 0);
-          }
-          tc5::mma_commit(&bars->s_full[x]);
+      const uint64_t dv = tc5::smem_desc(smem_u32(sm + kOffV), kUnitBox, 1024, tc5::kSwizzle128B);
+      bool ok = wait_or_abort(&bars->q_full, 0, abort_flag);
+      for (int j = j0 - 2; j < j1; ++j) {   // O += P V of unit j, S of unit j + 2
+        const unsigned vi = (unsigned)(j - j0), ki = vi + 2, i = (unsigned)(j - first);
+        const bool values = j >= j0, keys = j + 2 < j1, pv = j >= first && j < end;
+        uint64_t* bv = &bars->v_full[vi % kVStages];
+        uint64_t* bk = &bars->k_full[ki % kKStages];
+        uint64_t* bp = &bars->p_full[x][i & 1];
+        const uint32_t pv_par = (vi / kVStages) & 1, pk_par = (ki / kKStages) & 1, pp_par = (i >> 1) & 1;
+        if (!(values && keys && pv && peek3(bv, pv_par, bk, pk_par, bp, pp_par))) {
+          if (values) ok = ok && wait_or_abort(bv, pv_par, abort_flag);
+          if (keys) ok = ok && wait_or_abort(bk, pk_par, abort_flag);
+          if (pv) ok = ok && wait_or_abort(bp, pp_par, abort_flag);
         }
-      };
-      auto issue_o = [&](int x, int j) {   // O_x += P_x V_j
-        if (elect_one()) {
-          const uint64_t vs = dv + ((j - j0) % kVStages) * (kTileBytes >> 4);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)      // 16 keys: two 8-row groups of both 64-column boxes
-            mma_bf16_ta(tmem + kColO + 128 * x, tmem + kColS + 128 * x + 8 * c, vs + c * (2048 >> 4), idesc_o,
-                        j > t0[x] || c > 0);
-          if (j == t1[x] - 1) tc5::mma_commit(&bars->o_full[x]);
-        }
-      };
-      bool ok = wait_or_abort(&bars->q_full, 0, abort_flag) && wait_or_abort(&bars->k_full[0], 0, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc5::fence_after_sync();
-        for (int x = 0; x < 2; ++x)
-          if (t0[x] == j0) issue_s(x, j0);
-        if (elect_one()) tc5::mma_commit(&bars->k_empty[0]);
-      }
-      int done[2] = {0, 0};   // P tiles taken per block
-      for (int j = j0; ok && j < j1; ++j) {
-        const int vi = j - j0, ki = vi + 1;
-        const bool more = j + 1 < j1;
-        ok = wait_or_abort(&bars->v_full[vi % kVStages], (vi / kVStages) & 1, abort_flag);
-        if (ok && more) ok = wait_or_abort(&bars->k_full[ki % kKStages], (ki / kKStages) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const int valid = n_k - j * kTile;
-        if (valid < kTile) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
-          unsigned char* vs = sm + kOffV + (vi % kVStages) * kTileBytes;
-          for (int e = lane; e < (kTile - valid) * 16; e += 32) {
+        const int valid = n_k - j * kUnit;
+        if (values && valid < kUnit) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
+          unsigned char* vs = sm + kOffV + (vi % kVStages) * kUnitBytes;
+          for (int e = lane; e < (kUnit - valid) * 16; e += 32) {
             const int r = valid + (e >> 4), c = e & 15;
-            *reinterpret_cast<uint4*>(vs + (c >> 3) * kBoxBytes + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(vs + (c >> 3) * kUnitBox + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
           __syncwarp();
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (j >= t0[x] && j < t1[x]) {
-            ok = ok && wait_or_abort(&bars->p_full[x], done[x] & 1, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ++done[x];
-            tc5::fence_after_sync();
-            issue_o(x, j);
-          }
-          if (more && j + 1 >= t0[x] && j + 1 < t1[x]) issue_s(x, j + 1);
-        }
-        if (!ok) break;
+        tc5::fence_after_sync();
+        const bool scores = j + 2 >= first && j + 2 < end;
         if (elect_one()) {
-          tc5::mma_commit(&bars->v_empty[vi % kVStages]);
-          if (more) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
+          const uint32_t ti = ts + 64 * (i & 1);
+          if (pv) {   // 16 keys a step: two 8-row groups of both 64-column boxes
+            const uint64_t vs = dv + (vi % kVStages) * (kUnitBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mma_bf16_ta(to, ti + 8 * c, vs + c * (2048 >> 4), idesc_o, j > first || c > 0);
+          }
+          if (scores) {
+            const uint64_t ks = dk + (ki % kKStages) * (kUnitBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              tc5::mma_bf16(ti, dq + (((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4),
+                            ks + (((c >> 2) * kUnitBox + (c & 3) * 32) >> 4), idesc_s, c > 0);
+          }
+          // past the last unit the barrier still tells that O += P V is complete
+          if (scores || pv) tc5::mma_commit(&bars->s_full[x][i & 1]);
+          if (values) tc5::mma_commit(&bars->v_empty[vi % kVStages]);
+          if (keys) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
         }
+        __syncwarp();
       }
       // every MMA done before tensor memory is freed
       __syncwarp();
@@ -300,58 +331,68 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // softmax of block x, a thread per row = tensor-memory lane
     const int x = warp >> 2;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = lanes + kColS + 128 * x, to = lanes + kColO + 128 * x;
+    const uint32_t to = lanes + kColO + 128 * x;
     const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;   // reference (log2 units) and the sum of weights
     bool ok = true;
     const int nt = t1[x] - t0[x];
     for (int it = 0; it < nt; ++it) {
-      const int base = (t0[x] + it) * kTile;
-      ok = wait_or_abort(&bars->s_full[x], it & 1, abort_flag);
+      const int base = (t0[x] + it) * kUnit;
+      const uint32_t ts = lanes + kColS + 128 * x + 64 * (it & 1);
+      ok = wait_or_abort(&bars->s_full[x][it & 1], (it >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc5::fence_after_sync();
-      float s[kTile];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s + 32 * c);
+      float s[kUnit];
+      tmem_ld32(ts, s);
+      tmem_ld32(ts + 32, s + 32);
       tc5::tmem_wait_ld();
-      if (CAP) {   // softcap tanh(s / softcap) = softcap (1 - 2 / (1 + e^(2 s / softcap)))
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          s[c] = fmaf(-2.f * p.cap_log2, rcp_fast(1.f + ex2(s[c] * p.cap_in)), p.cap_log2);
-      }
-      if (BIAS) {
+      if (CAP) cap_scores(p, s);
+      if (BIAS) {   // s qk_log2 - slope |j - i|, without the bars where no key of the unit is behind a row
         const float off = (float)(base - pos);
+        const float mul = CAP ? 1.f : p.qk_log2;
+        if (__all_sync(0xffffffffu, off <= (float)(1 - kUnit))) {
+          const f32x2 m2 = pack2(mul, mul), sl2 = pack2(slope, slope), off2 = pack2(slope * off, slope * off);
 #pragma unroll
-        for (int c = 0; c < kTile; ++c) {
-          const float v = CAP ? s[c] : s[c] * p.qk_log2;
-          s[c] = fmaf(-slope, fabsf(off + (float)c), v);
+          for (int c = 0; c < kUnit; c += 2) {
+            const f32x2 bias = fma2(sl2, pack2((float)c, (float)(c + 1)), off2);
+            unpack2(fma2(pack2(s[c], s[c + 1]), m2, bias), s[c], s[c + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kUnit; ++c) s[c] = fmaf(-slope, fabsf(off + (float)c), s[c] * mul);
         }
       }
       const int lo_t = lo - base, hi_t = hi - base;
-      if (!__all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kTile - 1)) {
+      if (!__all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kUnit - 1)) {
 #pragma unroll
-        for (int c = 0; c < kTile; ++c)
+        for (int c = 0; c < kUnit; ++c)
           if (c < lo_t || c > hi_t) s[c] = -INFINITY;
       }
       float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
 #pragma unroll
-      for (int c = 4; c < kTile; c += 4) {
-        mx0 = fmaxf(mx0, s[c]);
-        mx1 = fmaxf(mx1, s[c + 1]);
-        mx2 = fmaxf(mx2, s[c + 2]);
-        mx3 = fmaxf(mx3, s[c + 3]);
+      for (int c = 4; c < kUnit - 4; c += 8) {
+        mx0 = max3(mx0, s[c], s[c + 4]);
+        mx1 = max3(mx1, s[c + 1], s[c + 5]);
+        mx2 = max3(mx2, s[c + 2], s[c + 6]);
+        mx3 = max3(mx3, s[c + 3], s[c + 7]);
       }
+      mx0 = max3(mx0, s[kUnit - 4], s[kUnit - 3]);
+      mx1 = max3(mx1, s[kUnit - 2], s[kUnit - 1]);
       constexpr bool kRaw = !CAP && !BIAS;   // s still lacks the factor qk_log2
       const float mul = kRaw ? p.qk_log2 : 1.f;
-      const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * mul;
+      const float mx = fmaxf(max3(mx0, mx1, mx2), mx3) * mul;
       const bool grow = mx > m + kLazy;
       if (__any_sync(0xffffffffu, grow)) {
         const float m_new = grow ? mx : m;
-        const float f = m_new == m ? 1.f : ex2(m - m_new);   // 0 for a row's first tile
+        const float f = m_new == m ? 1.f : ex2(m - m_new);   // 0 for a row's first unit
         m = m_new;
         l *= f;
         if (it > 0) {
+          const int nx = it + 1;   // scores of the next unit: the last product into O is complete
+          ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][nx & 1], (nx >> 1) & 1, abort_flag));
+          if (!ok) break;
+          tc5::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < kD; c += 32) {
             float o[32];
@@ -364,27 +405,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       const float sub = m == -INFINITY ? 0.f : -m;
-      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+      const f32x2 mul2v = pack2(mul, mul), sub2 = pack2(sub, sub);
+      f32x2 la = 0ull, lb = 0ull;
+      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < kTile; c += 64) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float p0 = ex2(fmaf(s[c + 2 * e], mul, sub)), p1 = ex2(fmaf(s[c + 2 * e + 1], mul, sub));
-          const float p2 = ex2(fmaf(s[c + 2 * e + 2], mul, sub)), p3 = ex2(fmaf(s[c + 2 * e + 3], mul, sub));
-          l0 += p0, l1 += p1, l2 += p2, l3 += p3;
-          w[e] = cvt_bf16x2(p0, p1);
-          w[e + 1] = cvt_bf16x2(p2, p3);
-        }
-        tmem_st32(ts + c / 2, w);
+      for (int e = 0; e < 32; e += 2) {
+        float p0, p1, p2, p3;
+        unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), mul2v, sub2), p0, p1);
+        unpack2(fma2(pack2(s[2 * e + 2], s[2 * e + 3]), mul2v, sub2), p2, p3);
+        p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+        la = add2(la, pack2(p0, p1));
+        lb = add2(lb, pack2(p2, p3));
+        w[e] = cvt_bf16x2(p0, p1);
+        w[e + 1] = cvt_bf16x2(p2, p3);
       }
-      l += (l0 + l1) + (l2 + l3);
+      tmem_st32(ts, w);
+      float l0, l1;
+      unpack2(add2(la, lb), l0, l1);
+      l += l0 + l1;
       tmem_wait_st();
       tc5::fence_before_sync();
-      mbar_arrive(&bars->p_full[x]);
+      mbar_arrive(&bars->p_full[x][it & 1]);
     }
     // out = O / l; zeros for a row that saw nothing
-    if (nt > 0 && ok) ok = __all_sync(0xffffffffu, wait_or_abort(&bars->o_full[x], 0, abort_flag));
+    if (nt > 0 && ok)
+      ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][(nt + 1) & 1], ((nt + 1) >> 1) & 1, abort_flag));
     if (ok) {
       tc5::fence_after_sync();
       const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -14,16 +14,18 @@
 // each, two groups of four warps do the softmax of a block each.  When a block's P of
 // unit u arrives its MMA warp issues O += P V of u and S of unit u + 2, so the group
 // finds the scores of u + 1 ready: the tensor cores run beside the softmax of the same
-// block, not only of the other one.  (One MMA warp for both blocks: 689 us where 511
-// had been with units of 128 keys; it spent 1200 clocks a unit on its four waits.)
+// block, not only of the other one.  
 //
 // Bound: a unit of both blocks costs 2 x 2 x 2 x 128 x 64 x 128 tensor flops and
 // 2 x 128 x 64 exponentials; at 8192 flops and 16 exponentials a clock and SM both take
 // 1024 clocks (1148 measured for the products: S with N = 64 reads shared memory at
-// 48 clocks per step where 32 would do), so the softmax's instruction count decides:
-// two-wide fp32 instructions, three-input maxima.  With units of 128 keys (S and P in
-// the same columns, so S of the next unit waited for O += P V of this one) 8192 causal
-// tokens x 32 heads took 511 us.
+// 48 clocks per step where 32 would do).  The groups compute their exponentials in
+// turn, 770 clocks a unit each, beside the other group's loads, maxima and stores: a
+// unit of both blocks takes 1555 clocks, and a CTA 11000 more before its first and after
+// its last one.  8192 causal tokens x 32 heads: 473 us (1161 TFLOP/s at 1.66 GHz, the
+// power limit's clock); with tiles of 128 keys, whose S has to wait for O += P V of the
+// tile before, 511 us; with one MMA warp for both blocks, whose waits at four barriers a
+// unit took 1200 clocks, 689 us; without the turns 485 us.
 //
 // The running reference m only moves when a row's maximum passes it by more than
 // 2^8 (weights then stay below 2^8, and the row's sum is in fp32): O is rescaled
@@ -93,6 +95,7 @@ struct Bars {
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2][2], p_full[2][2];   // [block][unit & 1]
+  uint64_t tail_full;                    // values of a last unit that ends inside it, before they are cleared
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -134,6 +137,23 @@ __device__ __forceinline__ void cap_scores(const Params& p, float (&s)[kUnit]) {
   }
 }
 
+// Weights 2^(s mul + sub) of a row's unit as packed bf16, and the two halves of their sum
+// before rounding.  (A quarter or half of them by a cubic polynomial on the fp32 pipe, which
+// has 10 clocks of work for what the special-function unit does in 8: no faster.)
+__device__ __forceinline__ f32x2 weights(const float (&s)[kUnit], float mul, float sub, uint32_t (&w)[32]) {
+  const f32x2 m2 = pack2(mul, mul), sub2 = pack2(sub, sub);
+  f32x2 sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    float p0, p1;
+    unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), m2, sub2), p0, p1);
+    p0 = ex2(p0), p1 = ex2(p1);
+    sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+    w[e] = cvt_bf16x2(p0, p1);
+  }
+  return add2(sum[0], sum[1]);
+}
+
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -171,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       bars->lo[x] = 0x7fffffff;
       bars->hi[x] = -1;
     }
+    mbar_init(&bars->tail_full, 1);
     mbar_init(&bars->drain, 2);
     bars->abort = 0;
     fence_mbar_init();
@@ -224,6 +245,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int j0 = min(t0[0], t0[1]), j1 = max(t1[0], t1[1]);
 
   if (warp == kTmaWarp) {
+    const int tail = n_k / kUnit;   // the unit that the sequence ends inside of
+    const bool clear = n_k % kUnit != 0 && tail >= j0 && tail < j1;
+    unsigned char* tail_v = sm + kOffV + (unsigned)(tail - j0) % kVStages * kUnitBytes;
+    bool ok = true;
     if (lane == 0 && j0 < j1) {
       mbar_arrive_expect_tx(&bars->q_full, 2 * kTileBytes);
 #pragma unroll
@@ -234,26 +259,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int r = 0; r < 2; ++r)
             tma_load_4d(sm + kOffQ + x * kTileBytes + c * kBoxBytes + r * kUnitBox, &p.map_q, 64 * c, h,
                         row0 + x * kTile + r * kUnit, b, &bars->q_full);
-      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, int off, int ns, int j) {
+      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, int off, int ns, int j, uint64_t* bar) {
         const int i = j - j0, s = i % ns;
         if (i >= ns && !wait_or_abort(&empty[s], ((i / ns) - 1) & 1, abort_flag)) return false;
-        mbar_arrive_expect_tx(&full[s], kUnitBytes);
+        if (!bar) bar = &full[s];
+        mbar_arrive_expect_tx(bar, kUnitBytes);
         unsigned char* dst = sm + off + s * kUnitBytes;
-        tma_load_4d(dst, map, 0, hk, j * kUnit, b, &full[s]);
-        tma_load_4d(dst + kUnitBox, map, 64, hk, j * kUnit, b, &full[s]);
+        tma_load_4d(dst, map, 0, hk, j * kUnit, b, bar);
+        tma_load_4d(dst + kUnitBox, map, 64, hk, j * kUnit, b, bar);
         return true;
       };
       int nk = 0, nv = 0;   // units loaded
-      bool ok = true;
       for (int j = j0 - 2; ok && j < j1; ++j) {
         if (j + 2 < j1) {
-          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 2);
+          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 2, nullptr);
           if (!ok) break;
           ++nk;
         }
         if (j < j0) continue;
-        ok = load(&p.map_v, bars->v_full, bars->v_empty, kOffV, kVStages, j);
-        if (ok) ++nv;
+        const bool last = clear && j == tail;   // the last unit of all, if it is one of them
+        ok = load(&p.map_v, bars->v_full, bars->v_empty, kOffV, kVStages, j, last ? &bars->tail_full : nullptr);
+        if (ok && !last) ++nv;
+        if (ok && last) ok = wait_or_abort(&bars->tail_full, 0, abort_flag);
       }
       // leave no copy in flight: wait for the last fill of every stage
       mbar_wait_bounded(&bars->q_full, 0, kWaitIters);
@@ -262,8 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int i = nv > kVStages ? nv - kVStages : 0; i < nv; ++i)
         mbar_wait_bounded(&bars->v_full[i % kVStages], (i / kVStages) & 1, kWaitIters);
     }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok && clear) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
+      const int valid = n_k % kUnit;
+      for (int e = lane; e < (kUnit - valid) * 16; e += 32) {
+        const int r = valid + (e >> 4), c = e & 15;
+        *reinterpret_cast<uint4*>(tail_v + (c >> 3) * kUnitBox + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->v_full[(unsigned)(tail - j0) % kVStages]);
+    }
   } else if (warp >= kMmaWarp) {
-    if (j0 < j1) {
+    if (j0 < j1 && elect_one()) {   // one thread does it all
       const int x = warp - kMmaWarp, first = x ? t0[1] : t0[0], end = x ? t1[1] : t1[0];
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kTile, kUnit);
       constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kTile, kD);
@@ -273,60 +311,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint64_t dk = tc5::smem_desc(smem_u32(sm + kOffK), 16, 1024, tc5::kSwizzle128B);
       const uint64_t dv = tc5::smem_desc(smem_u32(sm + kOffV), kUnitBox, 1024, tc5::kSwizzle128B);
       bool ok = wait_or_abort(&bars->q_full, 0, abort_flag);
+      // A look at a barrier takes 90 clocks, beside busy warps up to 300: a step's values and keys are
+      // waited for before its P can be there, so that only the wait for P stands in its way.
+      auto ready = [&](int j) {
+        const unsigned vi = (unsigned)(j - j0), ki = vi + 2;
+        if (j + 2 < j1) ok = ok && wait_or_abort(&bars->k_full[ki % kKStages], (ki / kKStages) & 1, abort_flag);
+        if (j >= j0 && j < j1) ok = ok && wait_or_abort(&bars->v_full[vi % kVStages], (vi / kVStages) & 1, abort_flag);
+      };
+      ready(j0 - 2);
       for (int j = j0 - 2; j < j1; ++j) {   // O += P V of unit j, S of unit j + 2
         const unsigned vi = (unsigned)(j - j0), ki = vi + 2, i = (unsigned)(j - first);
         const bool values = j >= j0, keys = j + 2 < j1, pv = j >= first && j < end;
-        uint64_t* bv = &bars->v_full[vi % kVStages];
-        uint64_t* bk = &bars->k_full[ki % kKStages];
-        uint64_t* bp = &bars->p_full[x][i & 1];
-        const uint32_t pv_par = (vi / kVStages) & 1, pk_par = (ki / kKStages) & 1, pp_par = (i >> 1) & 1;
-        if (!(values && keys && pv && peek3(bv, pv_par, bk, pk_par, bp, pp_par))) {
-          if (values) ok = ok && wait_or_abort(bv, pv_par, abort_flag);
-          if (keys) ok = ok && wait_or_abort(bk, pk_par, abort_flag);
-          if (pv) ok = ok && wait_or_abort(bp, pp_par, abort_flag);
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        if (pv) ok = ok && wait_or_abort(&bars->p_full[x][i & 1], (i >> 1) & 1, abort_flag);
         if (!ok) break;
-        const int valid = n_k - j * kUnit;
-        if (values && valid < kUnit) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
-          unsigned char* vs = sm + kOffV + (vi % kVStages) * kUnitBytes;
-          for (int e = lane; e < (kUnit - valid) * 16; e += 32) {
-            const int r = valid + (e >> 4), c = e & 15;
-            *reinterpret_cast<uint4*>(vs + (c >> 3) * kUnitBox + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         tc5::fence_after_sync();
         const bool scores = j + 2 >= first && j + 2 < end;
-        if (elect_one()) {
-          const uint32_t ti = ts + 64 * (i & 1);
-          if (pv) {   // 16 keys a step: two 8-row groups of both 64-column boxes
-            const uint64_t vs = dv + (vi % kVStages) * (kUnitBytes >> 4);
+        const uint32_t ti = ts + 64 * (i & 1);
+        if (pv) {   // 16 keys a step: two 8-row groups of both 64-column boxes
+          const uint64_t vs = dv + (vi % kVStages) * (kUnitBytes >> 4);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              mma_bf16_ta(to, ti + 8 * c, vs + c * (2048 >> 4), idesc_o, j > first || c > 0);
-          }
-          if (scores) {
-            const uint64_t ks = dk + (ki % kKStages) * (kUnitBytes >> 4);
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              tc5::mma_bf16(ti, dq + (((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4),
-                            ks + (((c >> 2) * kUnitBox + (c & 3) * 32) >> 4), idesc_s, c > 0);
-          }
-          // past the last unit the barrier still tells that O += P V is complete
-          if (scores || pv) tc5::mma_commit(&bars->s_full[x][i & 1]);
-          if (values) tc5::mma_commit(&bars->v_empty[vi % kVStages]);
-          if (keys) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
+          for (int c = 0; c < 4; ++c)
+            mma_bf16_ta(to, ti + 8 * c, vs + c * (2048 >> 4), idesc_o, j > first || c > 0);
         }
-        __syncwarp();
+        if (scores) {
+          const uint64_t ks = dk + (ki % kKStages) * (kUnitBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tc5::mma_bf16(ti, dq + (((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4),
+                          ks + (((c >> 2) * kUnitBox + (c & 3) * 32) >> 4), idesc_s, c > 0);
+          }
+        }
+        // past the last unit the barrier still tells that O += P V is complete
+        if (scores || pv) tc5::mma_commit(&bars->s_full[x][i & 1]);
+        if (values) tc5::mma_commit(&bars->v_empty[vi % kVStages]);
+        if (keys) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
+        ready(j + 1);
       }
       // every MMA done before tensor memory is freed
-      __syncwarp();
-      if (elect_one()) tc5::mma_commit(&bars->drain);
+      tc5::mma_commit(&bars->drain);
       mbar_wait_bounded(&bars->drain, 0, kWaitIters);
-      __syncwarp();
     }
+    __syncwarp();
   } else {
     // softmax of block x, a thread per row = tensor-memory lane
     const int x = warp >> 2;
@@ -336,12 +361,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     float m = -INFINITY, l = 0.f;   // reference (log2 units) and the sum of weights
     bool ok = true;
     const int nt = t1[x] - t0[x];
-    for (int it = 0; it < nt; ++it) {
-      const int base = (t0[x] + it) * kUnit;
+    // The groups compute exponentials in turn (named barriers 1 and 2), unit by unit of both
+    // blocks: what else a unit takes runs beside the other group's exponentials.
+    auto my_turn = [&]() { tc5::named_bar_sync(1 + x, 2 * kTile); };
+    auto your_turn = [&](int j) {
+      if (x == 0 || j + 1 < j1) tc5::named_bar_arrive(2 - x, 2 * kTile);
+    };
+    if (x == 1 && j0 < j1) tc5::named_bar_arrive(1, 2 * kTile);
+    bool seen = false;   // this unit's scores are known to be there
+    for (int j = j0; j < j1; ++j) {
+      const int it = j - t0[x], base = j * kUnit;
       const uint32_t ts = lanes + kColS + 128 * x + 64 * (it & 1);
-      ok = wait_or_abort(&bars->s_full[x][it & 1], (it >> 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      const bool here = it >= 0 && it < nt;
+      if (here && !seen) ok = __all_sync(0xffffffffu, ok && wait_or_abort(&bars->s_full[x][it & 1], (it >> 1) & 1, abort_flag));
+      if (!here || !ok) {   // both groups take every turn
+        my_turn();
+        your_turn(j);
+        continue;
+      }
       tc5::fence_after_sync();
       float s[kUnit];
       tmem_ld32(ts, s);
@@ -364,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       const int lo_t = lo - base, hi_t = hi - base;
-      if (!__all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kUnit - 1)) {
+      const bool whole = __all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kUnit - 1);
+      if (!whole) {
 #pragma unroll
         for (int c = 0; c < kUnit; ++c)
           if (c < lo_t || c > hi_t) s[c] = -INFINITY;
@@ -391,10 +429,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (it > 0) {
           const int nx = it + 1;   // scores of the next unit: the last product into O is complete
           ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][nx & 1], (nx >> 1) & 1, abort_flag));
-          if (!ok) break;
           tc5::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
+          for (int c = 0; ok && c < kD; c += 32) {
             float o[32];
             tmem_ld32(to + c, o);
             tc5::tmem_wait_ld();
@@ -405,23 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       const float sub = m == -INFINITY ? 0.f : -m;
-      const f32x2 mul2v = pack2(mul, mul), sub2 = pack2(sub, sub);
-      f32x2 la = 0ull, lb = 0ull;
       uint32_t w[32];
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float p0, p1, p2, p3;
-        unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), mul2v, sub2), p0, p1);
-        unpack2(fma2(pack2(s[2 * e + 2], s[2 * e + 3]), mul2v, sub2), p2, p3);
-        p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
-        la = add2(la, pack2(p0, p1));
-        lb = add2(lb, pack2(p2, p3));
-        w[e] = cvt_bf16x2(p0, p1);
-        w[e + 1] = cvt_bf16x2(p2, p3);
-      }
+      my_turn();
+      const f32x2 sum = weights(s, mul, sub, w);
+      your_turn(j);
+      // the next unit's scores are mostly there by now: the look at their barrier overlaps the stores
+      seen = __all_sync(0xffffffffu, mbar_test(&bars->s_full[x][(it + 1) & 1], ((it + 1) >> 1) & 1));
       tmem_st32(ts, w);
       float l0, l1;
-      unpack2(add2(la, lb), l0, l1);
+      unpack2(sum, l0, l1);
       l += l0 + l1;
       tmem_wait_st();
       tc5::fence_before_sync();

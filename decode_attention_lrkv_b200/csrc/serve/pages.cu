@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_move_kernel(const __grid_co
     const int d = p.dst[i];
     // an entry that did not hold has another source than the plan's, or is a second one with the same
     // source: it writes the same row, so the references are counted by the first one alone
-    if (!in_range(d, p.D.B) || from[d] != p.src[i] + 1) continue;
+    if (!in_range(d, p.D.B) || from[d] == 0 || from[d] != p.src[i] + 1) continue;
     bool first = true;
     for (int j = threadIdx.x; j < i; j += kMoveThreads) first &= p.dst[j] != d;
     if (!__syncthreads_and(first)) continue;

@@ -110,7 +110,9 @@ __device__ __forceinline__ int call_tokens(const int32_t* t_new_b, int b, int t_
 // zero between calls lies in front.
 constexpr int kMaxTq = 64;             // query tokens per sequence of lrkv_paged_attn
 constexpr int kMaxRowBlocks = 4;      // 8-row blocks that a CTA of lrkv_paged_attn holds
-constexpr int kRecFloats = kD + 2;    // a row's partial result: values, reference, sum
+// A row's partial result: values (rows 136 floats apart, so that the 4 rows of a quad of
+// lanes lie in different banks), reference, sum.
+constexpr int kRecRow = kD + 8, kRecFloats = kRecRow + 2;
 // Warps of a lrkv_paged_attn CTA that holds nb blocks of 8 query rows: as many as their
 // accumulators leave registers for.
 __host__ __device__ constexpr int attn_warps(int nb) { return nb == 1 ? 16 : 8; }

@@ -84,6 +84,14 @@ lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   p.g = dims->Hq / dims->Hkv;
   p.row_blocks = L.row_blocks;
   p.per_block = (p.g * t_q + L.row_blocks - 1) / L.row_blocks;
+  const uint32_t hr = (uint32_t)dims->Hkv * p.row_blocks;
+  int ceil_log2 = 0;
+  while ((1u << ceil_log2) < hr) ++ceil_log2;
+  if (hr > 1) {   // exact for numbers below 2^31
+    p.hr_mul = (uint32_t)(((1ull << (31 + ceil_log2)) + hr - 1) / hr);
+    p.hr_shift = ceil_log2 - 1;
+  }
+  p.g_mul = 65536u / p.g + 1;
   p.page_shift = dims->page == 16 ? 4 : dims->page == 32 ? 5 : dims->page == 64 ? 6 : 7;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (L.rows) {

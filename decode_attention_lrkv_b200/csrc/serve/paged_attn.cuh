@@ -52,6 +52,9 @@ struct AttnParams {
   float* recs;
   int layer, t_q, g, row_blocks, per_block;   // query rows per block (before padding)
   int window, page_shift;
+  uint32_t hr_mul;   // numbers below 2^31 divided by Hkv row_blocks > 1: umulhi(x, hr_mul) >> hr_shift
+  int hr_shift;
+  uint32_t g_mul;    // numbers below 2^10 divided by g: x g_mul >> 16
   float row_log2;    // scale * log2(e)
   float cap_in;      // 2 / softcap: exponent of e in tanh, per unit of a score (0: no cap)
   float cap_log2;    // softcap * log2(e)
@@ -68,12 +71,13 @@ template <int NB>
 struct AttnConfig {
   static constexpr int kWarps = attn_warps(NB), kThreads = 32 * kWarps;
   static constexpr int kUnits = NB == 1 ? 3 : NB == 4 ? 4 : 5;   // ring of a warp, in units
-  static constexpr bool kQShared = NB > 2;    // query fragments in shared memory instead of registers
+  static constexpr bool kQShared = NB > 1;    // query fragments in shared memory instead of registers
   static constexpr int kQBytes = kQShared ? NB * 2048 : 0;
   static constexpr int kRows = 8 * NB, kRec = kRows * kRecFloats;
   static constexpr int kWarpBytes = kUnits * kUnitBytes + kQBytes;
   static_assert(kRec * 4 <= kWarpBytes, "a warp's last record lies in its ring");
   struct Row2 {           // rows 2 t4 and 2 t4 + 1 of an 8-row block
+    float s0[2];          // what the sums of keys' products start from
     float mul[2], slope[2], pos[2];
     int lo[2], hi[2];
   };
@@ -127,42 +131,73 @@ struct Place {
   int seg;               // number of the segment's first tile
 };
 
-// prefix: tiles before every group of per_thread sequences; n groups, n + 1 entries, n % 32 == 0.
-__device__ __forceinline__ Place locate(const AttnParams& p, const int* prefix, int n, int x, int per_thread, int hr_n,
-                                        int lane) {
-  const int unit = x / hr_n, step = n / 32;      // prefix <= x / hr_n  <=>  prefix * hr_n <= x
-  const int hi = __popc(__ballot_sync(0xffffffffu, prefix[lane * step] <= unit)) - 1;
-  const int lo = __popc(__ballot_sync(0xffffffffu, lane < step && prefix[hi * step + lane] <= unit)) - 1;
-  const int group = hi * step + lo;              // the last group that starts at or before x
-  Place at;
-  at.b = group * per_thread;
-  int before = prefix[group] * hr_n;
-  uint32_t st = 0;
-  for (;; ++at.b) {
-    at.s = sequence(p, at.b, &st);
-    const int all = at.s.tiles * hr_n;
-    if (x < before + all || at.b + 1 >= p.D.B) break;
-    before += all;
-  }
-  const int off = x - before, tiles = max(at.s.tiles, 1);
-  at.hr = off / tiles;
-  at.tile = off - at.hr * tiles;
-  at.seg = before + at.hr * tiles;
-  return at;
+// a / b for 0 <= a < 2^31 and a quotient below 2^22: the fp32 quotient is off by one at most.
+__device__ __forceinline__ int div_small(int a, int b, float inv_b) {
+  int q = (int)((float)a * inv_b);
+  const int r = a - q * b;
+  q += r >= b;
+  q -= r < 0;
+  return q;
 }
 
-// x tiles cut into n equal runs: run i is [start(i), start(i + 1)).  n < 2^15.
+// The sequences' tiles, so that tile numbers can be looked up: with up to 32 sequences every
+// warp holds them in its lanes, else shared memory holds the tiles before every group of
+// per_thread sequences (n groups, n + 1 entries, n % 32 == 0).
+struct Index {
+  const int* prefix;
+  int n, per_thread, hr_n;
+  Seq mine;       // up to 32 sequences: this lane's
+  int before;     // tiles of one kv head and row block before it
+
+  __device__ __forceinline__ Place locate(const AttnParams& p, int x, int lane) const {
+    const int unit = hr_n == 1 ? x : (int)(__umulhi((uint32_t)x, p.hr_mul) >> p.hr_shift);
+    Place at;
+    int first;   // tiles before the sequence
+    if (p.D.B <= 32) {   // the last sequence that starts at or before x and is not empty
+      at.b = 31 - __clz(__ballot_sync(0xffffffffu, before <= unit && mine.tiles > 0));
+      at.s.n_rows = __shfl_sync(0xffffffffu, mine.n_rows, at.b);
+      at.s.total = __shfl_sync(0xffffffffu, mine.total, at.b);
+      at.s.start = __shfl_sync(0xffffffffu, mine.start, at.b);
+      at.s.tile0 = __shfl_sync(0xffffffffu, mine.tile0, at.b);
+      at.s.tiles = __shfl_sync(0xffffffffu, mine.tiles, at.b);
+      first = __shfl_sync(0xffffffffu, before, at.b) * hr_n;
+    } else {
+      const int step = n / 32;             // prefix <= x / hr_n  <=>  prefix * hr_n <= x
+      const int hi = __popc(__ballot_sync(0xffffffffu, prefix[lane * step] <= unit)) - 1;
+      const int lo = __popc(__ballot_sync(0xffffffffu, lane < step && prefix[hi * step + lane] <= unit)) - 1;
+      const int group = hi * step + lo;    // the last group that starts at or before x
+      at.b = group * per_thread;
+      first = prefix[group] * hr_n;
+      uint32_t st = 0;
+      for (;; ++at.b) {
+        at.s = sequence(p, at.b, &st);
+        const int all = at.s.tiles * hr_n;
+        if (x < first + all || at.b + 1 >= p.D.B) break;
+        first += all;
+      }
+    }
+    const int off = x - first, tiles = max(at.s.tiles, 1);
+    at.hr = div_small(off, tiles, __fdividef(1.f, (float)tiles));
+    at.tile = off - at.hr * tiles;
+    at.seg = first + at.hr * tiles;
+    return at;
+  }
+};
+
+// x tiles cut into n equal runs: run i is [start(i), start(i + 1)).  n < 2^11.
 struct Runs {
-  unsigned n, quot, rest;
-  float per_tile;   // runs per tile, nearly
-  __device__ __forceinline__ Runs(int x, int runs)
-      : n(runs), quot((unsigned)x / runs), rest((unsigned)x % runs), per_tile((float)runs / (float)x) {}
-  __device__ __forceinline__ int start(int i) const { return (int)(quot * i + rest * i / n); }
+  int n, quot, rest;
+  float inv_n, per_tile;   // 1 / n; runs per tile, nearly
+  __device__ __forceinline__ Runs(int x, int runs) : n(runs), quot(x / runs), rest(x - quot * runs) {
+    inv_n = __fdividef(1.f, (float)runs);
+    per_tile = __fdividef((float)runs, (float)x);
+  }
+  __device__ __forceinline__ int start(int i) const { return quot * i + div_small(rest * i, n, inv_n); }
   // the run that tile t lies in (x > 0)
   __device__ __forceinline__ int of(int t) const {
-    int i = min((int)((float)t * per_tile), (int)n - 1);   // off by one at most
+    int i = min((int)((float)t * per_tile), n - 1);   // off by one at most
     while (start(i) > t) --i;
-    while (i + 1 < (int)n && start(i + 1) <= t) ++i;
+    while (i + 1 < n && start(i + 1) <= t) ++i;
     return i;
   }
 };
@@ -232,7 +267,7 @@ struct Producer {
       status |= LRKV_DEV_BAD_PAGE;
       return kNoPage;
     }
-    const unsigned ph = ((unsigned)p.layer * p.D.n_pages + id) * p.D.Hkv + (unsigned)at.hr / p.row_blocks;
+    const unsigned ph = ((unsigned)p.layer * p.D.n_pages + id) * p.D.Hkv + (unsigned)(p.row_blocks == 1 ? at.hr : at.hr / p.row_blocks);
     return (int)((ph << p.page_shift) + within);
   }
   __device__ __forceinline__ void load_rows(const AttnParams& p, int lane) {
@@ -245,13 +280,13 @@ struct Producer {
     if (PT == 16 && pos + 16 < at.s.total) row_b = row_of(p, row[1], 0);
   }
   // Issues the next unit (all lanes call it).
-  __device__ __forceinline__ void issue(const AttnParams& p, typename C::Shared& sh, int per_thread, int hr_n,
+  __device__ __forceinline__ void issue(const AttnParams& p, typename C::Shared& sh, const Index& index,
                                         unsigned char* ring, int warp, int lane) {
     if (!values) {
       if (at.tile >= at.s.tiles || at.tile - rows_at >= 32) {
         if (at.tile >= at.s.tiles) {
-          if (at.hr + 1 < hr_n) ++at.hr, at.tile = 0;     // the sequence's next head
-          else at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
+          if (at.hr + 1 < index.hr_n) ++at.hr, at.tile = 0;     // the sequence's next head
+          else at = index.locate(p, x, lane);
         }
         load_rows(p, lane);
       }
@@ -314,7 +349,8 @@ __device__ __forceinline__ void ldsm_x4_t_at(uint32_t (&r)[4], uint32_t addr) {
 
 // Where the row `rho` (token * g + head within the group) of kv head h goes.
 __device__ __forceinline__ size_t row_offset(const AttnParams& p, int b, int h, int rho) {
-  return (((size_t)b * p.t_q + rho / p.g) * p.D.Hq + h * p.g + rho % p.g) * kD;
+  const int tok = (int)((uint32_t)rho * p.g_mul >> 16);
+  return (((size_t)b * p.t_q + tok) * p.D.Hq + h * p.g + (rho - tok * p.g)) * kD;
 }
 
 // The place of bit number i of the set bits of a mask.
@@ -331,16 +367,17 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int i) {
 // Lane i holds record i's address.
 __device__ __forceinline__ void join_row(int n, const float* rec, int rows, int row, int lane, float4& o, float& m,
                                          float& l) {
-  const float mi = lane < n ? rec[rows * kD + row] : -INFINITY, li = lane < n ? rec[rows * kD + rows + row] : 0.f;
+  const float* at = rec + rows * kRecRow + row;
+  const float mi = lane < n ? at[0] : -INFINITY, li = lane < n ? at[rows] : 0.f;
   m = warp_max(mi);
   const float w = ex2(mi - (m == -INFINITY ? 0.f : m));   // 0 for lanes past n
   l = warp_sum(w * li);
   o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const float wi = __shfl_sync(0xffffffffu, w, i);
     const float* ri = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec), i));
-    const float4 v = *reinterpret_cast<const float4*>(ri + row * kD + 4 * lane);
+    const float4 v = *reinterpret_cast<const float4*>(ri + row * kRecRow + 4 * lane);
     o.x = fmaf(wi, v.x, o.x), o.y = fmaf(wi, v.y, o.y), o.z = fmaf(wi, v.z, o.z), o.w = fmaf(wi, v.w, o.w);
   }
 }
@@ -354,7 +391,7 @@ __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, floa
 template <int NB, int CODE, int PT>
 __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using C = AttnConfig<NB>;
-  constexpr int W = C::kWarps, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kD], references, sums
+  constexpr int W = C::kWarps, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kRecRow], references, sums
   constexpr bool kInt = CODE == LRKV_CODE_INT8;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm =
@@ -363,8 +400,6 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
   typename C::Shared& sh = *reinterpret_cast<typename C::Shared*>(sm + W * C::kWarpBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int hr_n = p.D.Hkv * p.row_blocks;
-  const int per_thread = (p.D.B + C::kThreads - 1) / C::kThreads;
   if (lane == 0) {
     for (int s = 0; s < C::kUnits; ++s) mbar_init(&sh.bars[warp][s], 2);
     fence_mbar_init();
@@ -379,38 +414,61 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
   griddep_wait();
   griddep_launch_dependents();
 
-  // tiles of one kv head and row block before every thread's sequences
+  Index index;
+  index.prefix = sh.prefix;
+  index.n = C::kThreads;
+  index.per_thread = (p.D.B + C::kThreads - 1) / C::kThreads;
+  index.hr_n = p.D.Hkv * p.row_blocks;
   uint32_t status = 0;
+  int T;
   {
     int n = 0;
-    const int b0 = tid * per_thread, b1 = min(b0 + per_thread, p.D.B);
-    for (int b = b0; b < b1; ++b) n += sequence(p, b, &status).tiles;
-    if (blockIdx.x != 0) status = 0;   // one CTA reports
+    if (p.D.B <= 32) {
+      index.mine.tiles = 0;
+      if (lane < p.D.B) index.mine = sequence(p, lane, &status);
+      n = index.mine.tiles;
+    } else {
+      const int b0 = tid * index.per_thread, b1 = min(b0 + index.per_thread, p.D.B);
+      for (int b = b0; b < b1; ++b) n += sequence(p, b, &status).tiles;
+    }
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (lane == 31) sh.warp_sum[warp] = sum;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-    sh.prefix[tid + 1] = before + sum;
-    if (tid == 0) sh.prefix[0] = 0;
-    __syncthreads();
+    index.before = sum - n;
+    T = __shfl_sync(0xffffffffu, sum, 31);
+    if (p.D.B > 32) {
+      if (lane == 31) sh.warp_sum[warp] = sum;
+      __syncthreads();
+      int before = 0;
+      for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+      sh.prefix[tid + 1] = before + sum;
+      if (tid == 0) sh.prefix[0] = 0;
+      __syncthreads();
+      T = sh.prefix[C::kThreads];
+    }
+    if (blockIdx.x != 0 || (p.D.B <= 32 && warp != 0)) status = 0;   // reported once
   }
-  const int T = sh.prefix[C::kThreads] * hr_n;
+  T *= index.hr_n;
   const int ctas = min((int)gridDim.x, (T + W - 1) / W);   // a tile per warp at least
   if ((int)blockIdx.x >= ctas) {
     if (status) atomicOr(p.C.dev_status, status);
     return;
   }
   const Runs workers(T, ctas * W);
-  const int X0 = workers.start(blockIdx.x * W), X1 = workers.start((blockIdx.x + 1) * W);
   unsigned char* ring = sm + warp * C::kWarpBytes;
   uint2* q_sh = reinterpret_cast<uint2*>(ring + C::kUnits * kUnitBytes);
 
+  // Four dims of every k-step of query row rho (zeros past the block's rows).
+  auto load_q = [&](const Place& at, int rho, int rho1, int h, uint2 (&w)[8]) {
+    if (rho < rho1) {
+      const lrkv_bf16* src = p.q + row_offset(p, at.b, h, rho) + 4 * t4;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint2*>(src + 16 * c);
+    }
+  };
   Producer<NB, PT> prod;
   prod.x = workers.start(blockIdx.x * W + warp);
   prod.end = workers.start(blockIdx.x * W + warp + 1);
@@ -423,13 +481,6 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
   uint32_t phase = 0;
   bool ok = true;
   Place at;
-  if (x < end) {
-    at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
-    prod.at = at;
-    prod.load_rows(p, lane);
-#pragma unroll 1
-    for (int s = 0; s < C::kUnits && prod.more(); ++s) prod.issue(p, sh, per_thread, hr_n, ring, warp, lane);
-  }
   int in_flight = min(C::kUnits, 2 * (end - x));
   // Waits for the next unit; on a time-out leaves no copy in flight.
   auto wait_unit = [&]() {
@@ -449,34 +500,41 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     slot = slot + 1 == C::kUnits ? 0 : slot + 1;
     phase ^= slot == 0;
     __syncwarp();
-    if (prod.more()) prod.issue(p, sh, per_thread, hr_n, ring, warp, lane);
+    if (prod.more()) prod.issue(p, sh, index, ring, warp, lane);
     else --in_flight;
   };
 
   for (bool first = true; x < end; first = false) {
-    if (!first) at = locate(p, sh.prefix, C::kThreads, x, per_thread, hr_n, lane);
-    const int h = at.hr / p.row_blocks, rb = at.hr % p.row_blocks;
+    at = index.locate(p, x, lane);
+    const int h = p.row_blocks == 1 ? at.hr : at.hr / p.row_blocks, rb = at.hr - h * p.row_blocks;
     const int n_tiles = min(at.s.tiles - at.tile, end - x);
     const int rho0 = rb * p.per_block, rho1 = min(min(rho0 + p.per_block, p.g * p.t_q), p.g * at.s.n_rows);
+    uint2 q_first[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) q_first[c] = make_uint2(0u, 0u);
+    load_q(at, rho0 + g8, rho1, h, q_first);
+    if (first) {   // beside the queries' way
+      prod.at = at;
+      prod.load_rows(p, lane);
+#pragma unroll 1
+      for (int s = 0; s < C::kUnits && prod.more(); ++s) prod.issue(p, sh, index, ring, warp, lane);
+    }
 
     // queries of the block as B fragments, scaled by a power of two per row so that the
     // row's largest element lies in [2^14, 2^15): f16 then keeps what is above 2^-28 of it
     uint32_t qf[C::kQShared ? 1 : NB][8][2];
-    float m[NB][2], l[NB][2], s0[NB][2];   // s0: what the sums of keys' products start from
+    float m[NB][2], l[NB][2];
     int all_lo = 0, all_hi = 0x7fffffff;   // keys that every row sees
     const uint32_t minus_shift[4] = {0xE480E480u, 0xE480E480u, 0xE480E480u, 0xE480E480u};   // f16x2 (-1152, -1152)
     __syncwarp();
 #pragma unroll
+    for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
+#pragma unroll 1
     for (int nb = 0; nb < NB; ++nb) {
-      const int rho = rho0 + 8 * nb + g8;
       uint2 w[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = make_uint2(0u, 0u);
-      if (rho < rho1) {
-        const lrkv_bf16* src = p.q + row_offset(p, at.b, h, rho) + 4 * t4;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint2*>(src + 16 * c);
-      }
+      for (int c = 0; c < 8; ++c) w[c] = nb == 0 ? q_first[c] : make_uint2(0u, 0u);
+      if (nb > 0) load_q(at, rho0 + 8 * nb + g8, rho1, h, w);
       uint32_t mag = 0;
 #pragma unroll
       for (int c = 0; c < 8; ++c) mag = __vmaxu2(mag, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu));
@@ -484,34 +542,29 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
       mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
       const int e = min(max((int)(mag >> 7), 15), 254) - 127;          // 2^e <= largest < 2^(e+1)
-      // 2^(14 - e) as two factors that are normal in fp32
-      const int up = 14 - e, up_a = up / 2;
-      const float fa = __uint_as_float((uint32_t)(127 + up_a) << 23), fb = __uint_as_float((uint32_t)(127 + up - up_a) << 23);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e), between 2^-113 and 2^126
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const uint32_t b0 = cvt_f16x2(bf_lo(w[c].x) * fa * fb, bf_hi(w[c].x) * fa * fb);
-        const uint32_t b1 = cvt_f16x2(bf_lo(w[c].y) * fa * fb, bf_hi(w[c].y) * fa * fb);
+        const uint32_t b0 = cvt_f16x2(bf_lo(w[c].x) * up, bf_hi(w[c].x) * up);
+        const uint32_t b1 = cvt_f16x2(bf_lo(w[c].y) * up, bf_hi(w[c].y) * up);
         if (kInt) mma_f16(acc, minus_shift, b0, b1, acc);
         if (C::kQShared) q_sh[(c * NB + nb) * 32 + lane] = make_uint2(b0, b1);
-        else qf[C::kQShared ? 0 : nb][c][0] = b0, qf[C::kQShared ? 0 : nb][c][1] = b1;
+        else qf[0][c][0] = b0, qf[0][c][1] = b1;
       }
       // this thread's score columns are rows 2 t4, 2 t4 + 1; lane t4 keeps what is known of them
       typename C::Row2 row;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        s0[nb][j] = acc[j];
+        row.s0[j] = acc[j];
         const int er = __shfl_sync(0xffffffffu, e, (2 * t4 + j) * 4);
-        const int down = er - 14, da = down / 2;
-        row.mul[j] = p.row_log2 * __uint_as_float((uint32_t)(127 + da) << 23) * __uint_as_float((uint32_t)(127 + down - da) << 23);
+        row.mul[j] = p.row_log2 * __uint_as_float((uint32_t)(127 + er - 14) << 23);   // 2^(e - 14) >= 2^-126
         const int r = rho0 + 8 * nb + 2 * t4 + j;
-        m[nb][j] = -INFINITY;
-        l[nb][j] = 0.f;
         row.lo[j] = 0;
         row.hi[j] = 0x7fffffff;
         row.pos[j] = row.slope[j] = 0.f;
         if (r < rho1) {
-          const int tok = r / p.g;
+          const int tok = (int)((uint32_t)r * p.g_mul >> 16);
           const size_t meta = (size_t)at.b * p.t_q + tok;
           const int i = at.s.start + tok;
           int a = p.first_key ? max(p.first_key[meta], 0) : 0, z = i;
@@ -525,7 +578,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           row.lo[j] = a;
           row.hi[j] = z;
           row.pos[j] = (float)i;
-          if (p.slopes) row.slope[j] = p.slopes[h * p.g + r % p.g] * kLog2e;
+          if (p.slopes) row.slope[j] = p.slopes[h * p.g + r - tok * p.g] * kLog2e;
           all_lo = max(all_lo, a);
           all_hi = min(all_hi, z);
         }
@@ -560,8 +613,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) s[nb][mt][k] = kInt ? s0[nb][k & 1] : 0.f;
-#pragma unroll
+          for (int k = 0; k < 4; ++k) s[nb][mt][k] = kInt ? sh.row[warp][nb][t4].s0[k & 1] : 0.f;
+#pragma unroll(C::kQShared ? 1 : 4)
       for (int c = 0; c < 8; c += 2) {
         uint32_t a[2][2][4];   // [16 dims][16 tokens]
 #pragma unroll
@@ -579,7 +632,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           for (int nb = 0; nb < NB; ++nb) {
             uint2 b;
             if (C::kQShared) b = q_sh[((c + i) * NB + nb) * 32 + lane];
-            else b = make_uint2(qf[C::kQShared ? 0 : nb][c + i][0], qf[C::kQShared ? 0 : nb][c + i][1]);
+            else b = make_uint2(qf[0][C::kQShared ? 0 : c + i][0], qf[0][C::kQShared ? 0 : c + i][1]);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
               mma_f16(s[nb][mt], a[i][mt], b.x, b.y, s[nb][mt]);
@@ -753,8 +806,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           const int r = 8 * nb + 2 * t4 + j;
 #pragma unroll
           for (int dt = 0; dt < 8; ++dt)
-            *reinterpret_cast<float2*>(rec + r * kD + 16 * dt + 2 * g8) = make_float2(o[nb][dt][j], o[nb][dt][2 + j]);
-          if (g8 == 0) rec[ROWS * kD + r] = m[nb][j], rec[ROWS * kD + ROWS + r] = l[nb][j];
+            *reinterpret_cast<float2*>(rec + r * kRecRow + 16 * dt + 2 * g8) = make_float2(o[nb][dt][j], o[nb][dt][2 + j]);
+          if (g8 == 0) rec[ROWS * kRecRow + r] = m[nb][j], rec[ROWS * kRecRow + ROWS + r] = l[nb][j];
         }
       if (lane == 0) {
         Piece& pc = sh.piece[warp][late];
@@ -777,6 +830,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     *rho0 = pc.hr % p.row_blocks * p.per_block;
     return min(min(*rho0 + p.per_block, p.g * p.t_q), p.g * call_tokens(p.t_q_b, pc.b, p.t_q, &st));
   };
+  const int X0 = workers.start(blockIdx.x * W), X1 = workers.start((blockIdx.x + 1) * W);
   // join the pieces of a segment: the warps that hold them share the rows
   for (int k = 0; k < 2; ++k) {
     const Piece mine = sh.piece[warp][k];
@@ -799,8 +853,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
       if (done) {
         store_row4(p.out + row_offset(p, mine.b, h, rho0 + row) + 4 * lane, o, l);
       } else {
-        *reinterpret_cast<float4*>(dst + row * kD + 4 * lane) = o;
-        if (lane == 0) dst[ROWS * kD + row] = m, dst[ROWS * kD + ROWS + row] = l;
+        *reinterpret_cast<float4*>(dst + row * kRecRow + 4 * lane) = o;
+        if (lane == 0) dst[ROWS * kRecRow + row] = m, dst[ROWS * kRecRow + ROWS + row] = l;
       }
     }
     if (!done && rank == 0 && lane == 0) sh.open[which] = mine;
@@ -831,10 +885,9 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     const int rho1 = piece_rows(first, &rho0, &h);
     const int n = c1 - c0 + 1;
     for (int row = warp; rho0 + row < rho1; row += W) {
-      // up to 32 records at a time
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       float m = -INFINITY, l = 0.f;
-      for (int i0 = 0; i0 < n; i0 += 32) {
+      for (int i0 = 0; i0 < n; i0 += 32) {   // up to 32 records at a time
         float4 o1;
         float m1, l1;
         const int i = min(i0 + lane, n - 1);

@@ -73,6 +73,7 @@ struct AttnConfig {
   static constexpr int kUnits = NB == 1 ? 3 : NB == 4 ? 4 : 5;   // ring of a warp, in units
   static constexpr bool kQShared = NB > 1;    // query fragments in shared memory instead of registers
   static constexpr int kQBytes = kQShared ? NB * 2048 : 0;
+  static constexpr int kJoin = NB == 1 ? 1 : 4;   // rows that a warp joins side by side
   static constexpr int kRows = 8 * NB, kRec = kRows * kRecFloats;
   static constexpr int kWarpBytes = kUnits * kUnitBytes + kQBytes;
   static_assert(kRec * 4 <= kWarpBytes, "a warp's last record lies in its ring");
@@ -363,22 +364,48 @@ __device__ __forceinline__ int nth_bit(uint32_t mask, int i) {
   }
   return at;
 }
-// Joins row `row` of n <= 32 records by a warp, four values to a lane: weights 2^(m_i - max m).
-// Lane i holds record i's address.
-__device__ __forceinline__ void join_row(int n, const float* rec, int rows, int row, int lane, float4& o, float& m,
-                                         float& l) {
-  const float* at = rec + rows * kRecRow + row;
-  const float mi = lane < n ? at[0] : -INFINITY, li = lane < n ? at[rows] : 0.f;
-  m = warp_max(mi);
-  const float w = ex2(mi - (m == -INFINITY ? 0.f : m));   // 0 for lanes past n
-  l = warp_sum(w * li);
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
+// Joins rows row0, row0 + step, .. (up to kJoin of them, below `stop`) of n <= 32 records by a
+// warp, four values of a row to a lane: weights 2^(m_i - max m).  Lane i holds record i's
+// address.  The rows go side by side: one after the other, the maxima and sums over lanes of
+// 32 rows took 22000 clocks.
+// (kJoin is 1 where a CTA holds 8 rows: a warp seldom has two, and 4 cost 3 us at 8K tokens.)
+template <int kJoin>
+__device__ __forceinline__ void join_rows(int n, const float* rec, int rows, int row0, int step, int stop, int lane,
+                                          float4 (&o)[kJoin], float (&m)[kJoin], float (&l)[kJoin]) {
+  const int cnt = kJoin == 1 ? 1 : min(kJoin, (stop - row0 + step - 1) / step);
+  float w[kJoin];
+  const float* at = rec + rows * kRecRow + row0;
+#pragma unroll
+  for (int k = 0; k < kJoin; ++k) {
+    w[k] = lane < n && k < cnt ? at[k * step] : -INFINITY;
+    l[k] = lane < n && k < cnt ? at[rows + k * step] : 0.f;
+    m[k] = w[k];
+    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], s));
+#pragma unroll
+  for (int k = 0; k < kJoin; ++k) {
+    w[k] = ex2(w[k] - (m[k] == -INFINITY ? 0.f : m[k]));   // 0 for lanes past n
+    l[k] *= w[k];
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) l[k] += __shfl_xor_sync(0xffffffffu, l[k], s);
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
-    const float wi = __shfl_sync(0xffffffffu, w, i);
     const float* ri = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec), i));
-    const float4 v = *reinterpret_cast<const float4*>(ri + row * kRecRow + 4 * lane);
-    o.x = fmaf(wi, v.x, o.x), o.y = fmaf(wi, v.y, o.y), o.z = fmaf(wi, v.z, o.z), o.w = fmaf(wi, v.w, o.w);
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      if (k >= cnt) break;
+      const float wi = __shfl_sync(0xffffffffu, w[k], i);
+      const float4 v = *reinterpret_cast<const float4*>(ri + (row0 + k * step) * kRecRow + 4 * lane);
+      o[k].x = fmaf(wi, v.x, o[k].x), o[k].y = fmaf(wi, v.y, o[k].y);
+      o[k].z = fmaf(wi, v.z, o[k].z), o[k].w = fmaf(wi, v.w, o[k].w);
+    }
   }
 }
 __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, float l) {
@@ -391,7 +418,7 @@ __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, floa
 template <int NB, int CODE, int PT>
 __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using C = AttnConfig<NB>;
-  constexpr int W = C::kWarps, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kRecRow], references, sums
+  constexpr int W = C::kWarps, kJoin = C::kJoin, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kRecRow], references, sums
   constexpr bool kInt = CODE == LRKV_CODE_INT8;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm =
@@ -846,15 +873,20 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     const bool done = mine.seg >= X0 && mine.seg + mine.tiles <= X1;
     const int which = mine.seg >= X0 ? 1 : 0;
     float* dst = p.recs + ((size_t)blockIdx.x * (2 + W) + which) * kRec;
-    for (int row = rank; rho0 + row < rho1; row += n) {
-      float4 o;
-      float m, l;
-      join_row(n, rec, ROWS, row, lane, o, m, l);
-      if (done) {
-        store_row4(p.out + row_offset(p, mine.b, h, rho0 + row) + 4 * lane, o, l);
-      } else {
-        *reinterpret_cast<float4*>(dst + row * kRecRow + 4 * lane) = o;
-        if (lane == 0) dst[ROWS * kRecRow + row] = m, dst[ROWS * kRecRow + ROWS + row] = l;
+    for (int row0 = rank; rho0 + row0 < rho1; row0 += kJoin * n) {
+      float4 o[kJoin];
+      float m[kJoin], l[kJoin];
+      join_rows(n, rec, ROWS, row0, n, rho1 - rho0, lane, o, m, l);
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        const int row = row0 + j * n;
+        if (rho0 + row >= rho1) continue;
+        if (done) {
+          store_row4(p.out + row_offset(p, mine.b, h, rho0 + row) + 4 * lane, o[j], l[j]);
+        } else {
+          *reinterpret_cast<float4*>(dst + row * kRecRow + 4 * lane) = o[j];
+          if (lane == 0) dst[ROWS * kRecRow + row] = m[j], dst[ROWS * kRecRow + ROWS + row] = l[j];
+        }
       }
     }
     if (!done && rank == 0 && lane == 0) sh.open[which] = mine;
@@ -884,21 +916,33 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     int rho0, h;
     const int rho1 = piece_rows(first, &rho0, &h);
     const int n = c1 - c0 + 1;
-    for (int row = warp; rho0 + row < rho1; row += W) {
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float m = -INFINITY, l = 0.f;
+    for (int row0 = warp; rho0 + row0 < rho1; row0 += kJoin * W) {
+      float4 o[kJoin];
+      float m[kJoin], l[kJoin];
       for (int i0 = 0; i0 < n; i0 += 32) {   // up to 32 records at a time
-        float4 o1;
-        float m1, l1;
+        float4 o1[kJoin];
+        float m1[kJoin], l1[kJoin];
         const int i = min(i0 + lane, n - 1);
         const float* rec = p.recs + ((size_t)(c0 + i) * (2 + W) + (i == 0 ? 1 : 0)) * kRec;
-        join_row(min(32, n - i0), rec, ROWS, row, lane, o1, m1, l1);
-        const float mm = fmaxf(m, m1), ref = mm == -INFINITY ? 0.f : mm, w = ex2(m - ref), w1 = ex2(m1 - ref);
-        o = make_float4(o.x * w + o1.x * w1, o.y * w + o1.y * w1, o.z * w + o1.z * w1, o.w * w + o1.w * w1);
-        l = l * w + l1 * w1;
-        m = mm;
+        join_rows(min(32, n - i0), rec, ROWS, row0, W, rho1 - rho0, lane, o1, m1, l1);
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) {
+          if (i0 == 0) {
+            o[j] = o1[j], m[j] = m1[j], l[j] = l1[j];
+            continue;
+          }
+          const float mm = fmaxf(m[j], m1[j]), ref = mm == -INFINITY ? 0.f : mm;
+          const float w = ex2(m[j] - ref), w1 = ex2(m1[j] - ref);
+          o[j] = make_float4(o[j].x * w + o1[j].x * w1, o[j].y * w + o1[j].y * w1, o[j].z * w + o1[j].z * w1,
+                             o[j].w * w + o1[j].w * w1);
+          l[j] = l[j] * w + l1[j] * w1;
+          m[j] = mm;
+        }
       }
-      store_row4(p.out + row_offset(p, first.b, h, rho0 + row) + 4 * lane, o, l);
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j)
+        if (rho0 + row0 + j * W < rho1)
+          store_row4(p.out + row_offset(p, first.b, h, rho0 + row0 + j * W) + 4 * lane, o[j], l[j]);
     }
   }
 }

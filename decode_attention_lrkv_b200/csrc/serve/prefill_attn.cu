@@ -49,13 +49,27 @@ lrkv_status check(const lrkv_prefill_dims* D) {
   return LRKV_OK;
 }
 
+// CTAs that share the keys of a pair of query blocks: one where the blocks fill the SMs;
+// else as many as fill them, with 6 units of keys for each at least, as a CTA's start and end
+// cost as much as 7 units and the join takes a launch.  (100 rows x 4 heads after 8000 keys:
+// 115 us in one piece, 21 us with 6 units at least, 23 with 8, 26 with 4.)
+int splits(const lrkv_prefill_dims& D) {
+  const long long ctas = ((long long)D.t_q + 2 * prefill::kTile - 1) / (2 * prefill::kTile) * D.Hq * D.B;
+  if (ctas == 0) return 1;
+  long long n = num_sms() / ctas;
+  const long long most = D.t_k / (6 * prefill::kUnit);
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)n;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t lrkv_prefill_workspace_size(const lrkv_prefill_dims* dims) {
-  (void)dims;
-  return 0;
+  if (check(dims) != LRKV_OK) return 0;
+  const int n = splits(*dims);
+  return n > 1 ? (size_t)n * dims->B * dims->Hq * dims->t_q * prefill::kPart * sizeof(float) : 0;
 }
 
 lrkv_status lrkv_prefill_attn(const lrkv_prefill_dims* dims, const lrkv_bf16* q, const lrkv_bf16* k,
@@ -71,8 +85,12 @@ lrkv_status lrkv_prefill_attn(const lrkv_prefill_dims* dims, const lrkv_bf16* q,
   const void* ptrs[] = {q, k, v, out, q_len, kv_len, dev_status, ws};
   for (const void* x : ptrs)
     if (!aligned16(x)) return LRKV_ERR_ALIGNMENT;
-  (void)ws_bytes;
   prefill::Params p = {};
+  p.n_split = splits(D);
+  if (p.n_split > 1) {
+    if (!ws || ws_bytes < lrkv_prefill_workspace_size(dims)) return LRKV_ERR_INVALID_ARG;
+    p.part = static_cast<float*>(ws);
+  }
   // no keys at all: the kernel writes zeros, its key and value maps are not used
   const int tk = D.t_k > 0 ? D.t_k : 1;
   if (!rows_map(&p.map_q, q, D.B, D.t_q, D.Hq, D.q_stride) ||
@@ -111,9 +129,12 @@ lrkv_status lrkv_prefill_attn(const lrkv_prefill_dims* dims, const lrkv_bf16* q,
   auto kern = cap ? (bias ? prefill::prefill_kernel<true, true> : prefill::prefill_kernel<true, false>)
                   : (bias ? prefill::prefill_kernel<false, true> : prefill::prefill_kernel<false, false>);
   if (!set_smem(kern, prefill::kSmemBytes)) return LRKV_ERR_CUDA;
-  const unsigned grid = (unsigned)((long long)p.n_blocks * D.Hq * D.B);
-  kern<<<grid, prefill::kThreads, prefill::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? LRKV_OK : LRKV_ERR_CUDA;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const long long grid = (long long)p.n_blocks * D.Hq * D.B * p.n_split;
+  st = launch_pdl(kern, dim3((unsigned)grid), dim3(prefill::kThreads), prefill::kSmemBytes, cs, p);
+  if (st != LRKV_OK || p.n_split == 1) return st;
+  const long long rows = (long long)D.B * D.Hq * D.t_q;
+  return launch_pdl(prefill::join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, cs, p);
 }
 
 }  // extern "C"

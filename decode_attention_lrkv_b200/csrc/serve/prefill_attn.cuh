@@ -14,18 +14,20 @@
 // each, two groups of four warps do the softmax of a block each.  When a block's P of
 // unit u arrives its MMA warp issues O += P V of u and S of unit u + 2, so the group
 // finds the scores of u + 1 ready: the tensor cores run beside the softmax of the same
-// block, not only of the other one.  
+// block, not only of the other one.  (One MMA warp for both blocks: 689 us where 511
+// had been with units of 128 keys; it spent 1200 clocks a unit on its four waits.)
 //
 // Bound: a unit of both blocks costs 2 x 2 x 2 x 128 x 64 x 128 tensor flops and
 // 2 x 128 x 64 exponentials; at 8192 flops and 16 exponentials a clock and SM both take
 // 1024 clocks (1148 measured for the products: S with N = 64 reads shared memory at
-// 48 clocks per step where 32 would do).  The groups compute their exponentials in
-// turn, 770 clocks a unit each, beside the other group's loads, maxima and stores: a
-// unit of both blocks takes 1555 clocks, and a CTA 11000 more before its first and after
-// its last one.  8192 causal tokens x 32 heads: 473 us (1161 TFLOP/s at 1.66 GHz, the
-// power limit's clock); with tiles of 128 keys, whose S has to wait for O += P V of the
-// tile before, 511 us; with one MMA warp for both blocks, whose waits at four barriers a
-// unit took 1200 clocks, 689 us; without the turns 485 us.
+// 48 clocks per step where 32 would do).  A unit of both blocks takes 1700 clocks, and a
+// CTA 11000 more before its first and after its last one.  8192 causal tokens x 32 heads:
+// 474 us (1160 TFLOP/s) at first, 545 us (1009) once the power limit has lowered the clock.
+// Also measured, each at first / under the power limit: the softmax groups taking their
+// exponentials in turn, one thread issuing all of a block's MMAs, 473 / 578 us; tiles of
+// 128 keys, whose S waits for O += P V of the tile before, 511 / 572; those with P in two
+// halves, 526 / 586; a quarter or half of the exponentials by a cubic polynomial, which is
+// 10 clocks of work on the fp32 pipe against 8 on the special-function unit, no faster.
 //
 // The running reference m only moves when a row's maximum passes it by more than
 // 2^8 (weights then stay below 2^8, and the row's sum is in fp32): O is rescaled
@@ -88,14 +90,17 @@ struct Params {
   float cap_log2;     // softcap * log2(e)
   float cap_poly[6];  // softcap log2(e) tanh(x) = x (cap_poly[0] + cap_poly[1] x^2 + ..), |x| <= 1
   int out32;          // 32-byte stores allowed
+  int n_split;        // CTAs that share a pair of query blocks' keys
+  float* part;        // n_split > 1: [n_split][B][Hq][t_q][kPart] results before the join
 };
+// A row's result of one split: O (not divided), the reference, the sum.
+constexpr int kPart = kD + 4;
 
 struct Bars {
   uint64_t q_full;
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2][2], p_full[2][2];   // [block][unit & 1]
-  uint64_t tail_full;                    // values of a last unit that ends inside it, before they are cleared
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -137,23 +142,6 @@ __device__ __forceinline__ void cap_scores(const Params& p, float (&s)[kUnit]) {
   }
 }
 
-// Weights 2^(s mul + sub) of a row's unit as packed bf16, and the two halves of their sum
-// before rounding.  (A quarter or half of them by a cubic polynomial on the fp32 pipe, which
-// has 10 clocks of work for what the special-function unit does in 8: no faster.)
-__device__ __forceinline__ f32x2 weights(const float (&s)[kUnit], float mul, float sub, uint32_t (&w)[32]) {
-  const f32x2 m2 = pack2(mul, mul), sub2 = pack2(sub, sub);
-  f32x2 sum[2] = {0ull, 0ull};
-#pragma unroll
-  for (int e = 0; e < 32; ++e) {
-    float p0, p1;
-    unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), m2, sub2), p0, p1);
-    p0 = ex2(p0), p1 = ex2(p1);
-    sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
-    w[e] = cvt_bf16x2(p0, p1);
-  }
-  return add2(sum[0], sum[1]);
-}
-
 template <bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -163,10 +151,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
+  griddep_wait();
+  griddep_launch_dependents();
   // the last query blocks first: under a causal mask they are the longest
-  const int hb = blockIdx.x % (p.Hq * p.B);
+  const int split = blockIdx.x % p.n_split, cta = blockIdx.x / p.n_split;
+  const int hb = cta % (p.Hq * p.B);
   const int h = hb % p.Hq, b = hb / p.Hq;
-  const int blk = p.n_blocks - 1 - blockIdx.x / (p.Hq * p.B);
+  const int blk = p.n_blocks - 1 - cta / (p.Hq * p.B);
   const int hk = h / (p.Hq / p.Hkv);
   int n_k = p.t_k, n_q = p.t_q;
   uint32_t bad = 0;
@@ -178,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     n_q = p.q_len[b];
     if (n_q < 0 || n_q > p.t_q) bad = LRKV_DEV_BAD_COUNT, n_q = n_q < 0 ? 0 : p.t_q;
   }
-  if (bad && p.dev_status && tid == 0 && blk == 0 && h == 0) atomicOr(p.dev_status, bad);
+  if (bad && p.dev_status && tid == 0 && blk == 0 && h == 0 && split == 0) atomicOr(p.dev_status, bad);
   const int row0 = blk * 2 * kTile;
   if (row0 >= n_q) return;
 
@@ -191,7 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       bars->lo[x] = 0x7fffffff;
       bars->hi[x] = -1;
     }
-    mbar_init(&bars->tail_full, 1);
     mbar_init(&bars->drain, 2);
     bars->abort = 0;
     fence_mbar_init();
@@ -242,13 +232,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     t0[x] = __shfl_sync(0xffffffffu, any ? bars->lo[x] / kUnit : 0x7ffffff0, 0);   // known to be uniform
     t1[x] = __shfl_sync(0xffffffffu, any ? bars->hi[x] / kUnit + 1 : 0, 0);
   }
+  if (p.n_split > 1) {   // this CTA's share of the units
+    const int first = min(t0[0], t0[1]), end = max(t1[0], t1[1]);
+    const int per = end > first ? (end - first + p.n_split - 1) / p.n_split : 0;
+    const int lo_u = first + split * per, hi_u = lo_u + per;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      t0[x] = max(t0[x], lo_u), t1[x] = min(t1[x], hi_u);
+      if (t0[x] >= t1[x]) t0[x] = 0x7ffffff0, t1[x] = 0;
+    }
+  }
   const int j0 = min(t0[0], t0[1]), j1 = max(t1[0], t1[1]);
 
   if (warp == kTmaWarp) {
-    const int tail = n_k / kUnit;   // the unit that the sequence ends inside of
-    const bool clear = n_k % kUnit != 0 && tail >= j0 && tail < j1;
-    unsigned char* tail_v = sm + kOffV + (unsigned)(tail - j0) % kVStages * kUnitBytes;
-    bool ok = true;
     if (lane == 0 && j0 < j1) {
       mbar_arrive_expect_tx(&bars->q_full, 2 * kTileBytes);
 #pragma unroll
@@ -259,28 +255,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int r = 0; r < 2; ++r)
             tma_load_4d(sm + kOffQ + x * kTileBytes + c * kBoxBytes + r * kUnitBox, &p.map_q, 64 * c, h,
                         row0 + x * kTile + r * kUnit, b, &bars->q_full);
-      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, int off, int ns, int j, uint64_t* bar) {
+      auto load = [&](const CUtensorMap* map, uint64_t* full, uint64_t* empty, int off, int ns, int j) {
         const int i = j - j0, s = i % ns;
         if (i >= ns && !wait_or_abort(&empty[s], ((i / ns) - 1) & 1, abort_flag)) return false;
-        if (!bar) bar = &full[s];
-        mbar_arrive_expect_tx(bar, kUnitBytes);
+        mbar_arrive_expect_tx(&full[s], kUnitBytes);
         unsigned char* dst = sm + off + s * kUnitBytes;
-        tma_load_4d(dst, map, 0, hk, j * kUnit, b, bar);
-        tma_load_4d(dst + kUnitBox, map, 64, hk, j * kUnit, b, bar);
+        tma_load_4d(dst, map, 0, hk, j * kUnit, b, &full[s]);
+        tma_load_4d(dst + kUnitBox, map, 64, hk, j * kUnit, b, &full[s]);
         return true;
       };
       int nk = 0, nv = 0;   // units loaded
+      bool ok = true;
       for (int j = j0 - 2; ok && j < j1; ++j) {
         if (j + 2 < j1) {
-          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 2, nullptr);
+          ok = load(&p.map_k, bars->k_full, bars->k_empty, kOffK, kKStages, j + 2);
           if (!ok) break;
           ++nk;
         }
         if (j < j0) continue;
-        const bool last = clear && j == tail;   // the last unit of all, if it is one of them
-        ok = load(&p.map_v, bars->v_full, bars->v_empty, kOffV, kVStages, j, last ? &bars->tail_full : nullptr);
-        if (ok && !last) ++nv;
-        if (ok && last) ok = wait_or_abort(&bars->tail_full, 0, abort_flag);
+        ok = load(&p.map_v, bars->v_full, bars->v_empty, kOffV, kVStages, j);
+        if (ok) ++nv;
       }
       // leave no copy in flight: wait for the last fill of every stage
       mbar_wait_bounded(&bars->q_full, 0, kWaitIters);
@@ -289,19 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int i = nv > kVStages ? nv - kVStages : 0; i < nv; ++i)
         mbar_wait_bounded(&bars->v_full[i % kVStages], (i / kVStages) & 1, kWaitIters);
     }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok && clear) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
-      const int valid = n_k % kUnit;
-      for (int e = lane; e < (kUnit - valid) * 16; e += 32) {
-        const int r = valid + (e >> 4), c = e & 15;
-        *reinterpret_cast<uint4*>(tail_v + (c >> 3) * kUnitBox + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->v_full[(unsigned)(tail - j0) % kVStages]);
-    }
   } else if (warp >= kMmaWarp) {
-    if (j0 < j1 && elect_one()) {   // one thread does it all
+    if (j0 < j1) {
       const int x = warp - kMmaWarp, first = x ? t0[1] : t0[0], end = x ? t1[1] : t1[0];
       constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kTile, kUnit);
       constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kTile, kD);
@@ -311,47 +294,60 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint64_t dk = tc5::smem_desc(smem_u32(sm + kOffK), 16, 1024, tc5::kSwizzle128B);
       const uint64_t dv = tc5::smem_desc(smem_u32(sm + kOffV), kUnitBox, 1024, tc5::kSwizzle128B);
       bool ok = wait_or_abort(&bars->q_full, 0, abort_flag);
-      // A look at a barrier takes 90 clocks, beside busy warps up to 300: a step's values and keys are
-      // waited for before its P can be there, so that only the wait for P stands in its way.
-      auto ready = [&](int j) {
-        const unsigned vi = (unsigned)(j - j0), ki = vi + 2;
-        if (j + 2 < j1) ok = ok && wait_or_abort(&bars->k_full[ki % kKStages], (ki / kKStages) & 1, abort_flag);
-        if (j >= j0 && j < j1) ok = ok && wait_or_abort(&bars->v_full[vi % kVStages], (vi / kVStages) & 1, abort_flag);
-      };
-      ready(j0 - 2);
       for (int j = j0 - 2; j < j1; ++j) {   // O += P V of unit j, S of unit j + 2
         const unsigned vi = (unsigned)(j - j0), ki = vi + 2, i = (unsigned)(j - first);
         const bool values = j >= j0, keys = j + 2 < j1, pv = j >= first && j < end;
-        if (pv) ok = ok && wait_or_abort(&bars->p_full[x][i & 1], (i >> 1) & 1, abort_flag);
+        uint64_t* bv = &bars->v_full[vi % kVStages];
+        uint64_t* bk = &bars->k_full[ki % kKStages];
+        uint64_t* bp = &bars->p_full[x][i & 1];
+        const uint32_t pv_par = (vi / kVStages) & 1, pk_par = (ki / kKStages) & 1, pp_par = (i >> 1) & 1;
+        if (!(values && keys && pv && peek3(bv, pv_par, bk, pk_par, bp, pp_par))) {
+          if (values) ok = ok && wait_or_abort(bv, pv_par, abort_flag);
+          if (keys) ok = ok && wait_or_abort(bk, pk_par, abort_flag);
+          if (pv) ok = ok && wait_or_abort(bp, pp_par, abort_flag);
+        }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        const int valid = n_k - j * kUnit;
+        if (values && valid < kUnit) {   // rows past the sequence may hold NaN, which a zero weight keeps: clear them
+          unsigned char* vs = sm + kOffV + (vi % kVStages) * kUnitBytes;
+          for (int e = lane; e < (kUnit - valid) * 16; e += 32) {
+            const int r = valid + (e >> 4), c = e & 15;
+            *reinterpret_cast<uint4*>(vs + (c >> 3) * kUnitBox + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         tc5::fence_after_sync();
         const bool scores = j + 2 >= first && j + 2 < end;
-        const uint32_t ti = ts + 64 * (i & 1);
-        if (pv) {   // 16 keys a step: two 8-row groups of both 64-column boxes
-          const uint64_t vs = dv + (vi % kVStages) * (kUnitBytes >> 4);
+        if (elect_one()) {
+          const uint32_t ti = ts + 64 * (i & 1);
+          if (pv) {   // 16 keys a step: two 8-row groups of both 64-column boxes
+            const uint64_t vs = dv + (vi % kVStages) * (kUnitBytes >> 4);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            mma_bf16_ta(to, ti + 8 * c, vs + c * (2048 >> 4), idesc_o, j > first || c > 0);
-        }
-        if (scores) {
-          const uint64_t ks = dk + (ki % kKStages) * (kUnitBytes >> 4);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tc5::mma_bf16(ti, dq + (((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4),
-                          ks + (((c >> 2) * kUnitBox + (c & 3) * 32) >> 4), idesc_s, c > 0);
+            for (int c = 0; c < 4; ++c)
+              mma_bf16_ta(to, ti + 8 * c, vs + c * (2048 >> 4), idesc_o, j > first || c > 0);
           }
+          if (scores) {
+            const uint64_t ks = dk + (ki % kKStages) * (kUnitBytes >> 4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              tc5::mma_bf16(ti, dq + (((c >> 2) * kBoxBytes + (c & 3) * 32) >> 4),
+                            ks + (((c >> 2) * kUnitBox + (c & 3) * 32) >> 4), idesc_s, c > 0);
+          }
+          // past the last unit the barrier still tells that O += P V is complete
+          if (scores || pv) tc5::mma_commit(&bars->s_full[x][i & 1]);
+          if (values) tc5::mma_commit(&bars->v_empty[vi % kVStages]);
+          if (keys) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
         }
-        // past the last unit the barrier still tells that O += P V is complete
-        if (scores || pv) tc5::mma_commit(&bars->s_full[x][i & 1]);
-        if (values) tc5::mma_commit(&bars->v_empty[vi % kVStages]);
-        if (keys) tc5::mma_commit(&bars->k_empty[ki % kKStages]);
-        ready(j + 1);
+        __syncwarp();
       }
       // every MMA done before tensor memory is freed
-      tc5::mma_commit(&bars->drain);
+      __syncwarp();
+      if (elect_one()) tc5::mma_commit(&bars->drain);
       mbar_wait_bounded(&bars->drain, 0, kWaitIters);
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // softmax of block x, a thread per row = tensor-memory lane
     const int x = warp >> 2;
@@ -360,25 +356,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const float slope = BIAS ? p.slopes[h] * kLog2e : 0.f;
     float m = -INFINITY, l = 0.f;   // reference (log2 units) and the sum of weights
     bool ok = true;
-    const int nt = t1[x] - t0[x];
-    // The groups compute exponentials in turn (named barriers 1 and 2), unit by unit of both
-    // blocks: what else a unit takes runs beside the other group's exponentials.
-    auto my_turn = [&]() { tc5::named_bar_sync(1 + x, 2 * kTile); };
-    auto your_turn = [&](int j) {
-      if (x == 0 || j + 1 < j1) tc5::named_bar_arrive(2 - x, 2 * kTile);
-    };
-    if (x == 1 && j0 < j1) tc5::named_bar_arrive(1, 2 * kTile);
-    bool seen = false;   // this unit's scores are known to be there
-    for (int j = j0; j < j1; ++j) {
-      const int it = j - t0[x], base = j * kUnit;
+    const int nt = t1[x] > t0[x] ? t1[x] - t0[x] : 0;
+    for (int it = 0; it < nt; ++it) {
+      const int base = (t0[x] + it) * kUnit;
       const uint32_t ts = lanes + kColS + 128 * x + 64 * (it & 1);
-      const bool here = it >= 0 && it < nt;
-      if (here && !seen) ok = __all_sync(0xffffffffu, ok && wait_or_abort(&bars->s_full[x][it & 1], (it >> 1) & 1, abort_flag));
-      if (!here || !ok) {   // both groups take every turn
-        my_turn();
-        your_turn(j);
-        continue;
-      }
+      ok = wait_or_abort(&bars->s_full[x][it & 1], (it >> 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc5::fence_after_sync();
       float s[kUnit];
       tmem_ld32(ts, s);
@@ -401,8 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       const int lo_t = lo - base, hi_t = hi - base;
-      const bool whole = __all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kUnit - 1);
-      if (!whole) {
+      if (!__all_sync(0xffffffffu, lo_t <= 0 && hi_t >= kUnit - 1)) {
 #pragma unroll
         for (int c = 0; c < kUnit; ++c)
           if (c < lo_t || c > hi_t) s[c] = -INFINITY;
@@ -429,9 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         if (it > 0) {
           const int nx = it + 1;   // scores of the next unit: the last product into O is complete
           ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][nx & 1], (nx >> 1) & 1, abort_flag));
+          if (!ok) break;
           tc5::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; ok && c < kD; c += 32) {
+          for (int c = 0; c < kD; c += 32) {
             float o[32];
             tmem_ld32(to + c, o);
             tc5::tmem_wait_ld();
@@ -442,15 +426,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       const float sub = m == -INFINITY ? 0.f : -m;
+      const f32x2 mul2v = pack2(mul, mul), sub2 = pack2(sub, sub);
+      f32x2 la = 0ull, lb = 0ull;
       uint32_t w[32];
-      my_turn();
-      const f32x2 sum = weights(s, mul, sub, w);
-      your_turn(j);
-      // the next unit's scores are mostly there by now: the look at their barrier overlaps the stores
-      seen = __all_sync(0xffffffffu, mbar_test(&bars->s_full[x][(it + 1) & 1], ((it + 1) >> 1) & 1));
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float p0, p1, p2, p3;
+        unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), mul2v, sub2), p0, p1);
+        unpack2(fma2(pack2(s[2 * e + 2], s[2 * e + 3]), mul2v, sub2), p2, p3);
+        p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+        la = add2(la, pack2(p0, p1));
+        lb = add2(lb, pack2(p2, p3));
+        w[e] = cvt_bf16x2(p0, p1);
+        w[e + 1] = cvt_bf16x2(p2, p3);
+      }
       tmem_st32(ts, w);
       float l0, l1;
-      unpack2(sum, l0, l1);
+      unpack2(add2(la, lb), l0, l1);
       l += l0 + l1;
       tmem_wait_st();
       tc5::fence_before_sync();
@@ -459,7 +451,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // out = O / l; zeros for a row that saw nothing
     if (nt > 0 && ok)
       ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][(nt + 1) & 1], ((nt + 1) >> 1) & 1, abort_flag));
-    if (ok) {
+    if (ok && p.n_split > 1) {
+      tc5::fence_after_sync();
+      float* rec = p.part + ((((size_t)split * p.B + b) * p.Hq + h) * p.t_q + row) * kPart;
+#pragma unroll 1
+      for (int c = 0; c < kD && nt > 0; c += 32) {
+        float o[32];
+        tmem_ld32(to + c, o);
+        tc5::tmem_wait_ld();
+        if (row < n_q) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(rec + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (row < n_q) rec[kD] = nt > 0 ? m : -INFINITY, rec[kD + 1] = l;
+    } else if (ok) {
       tc5::fence_after_sync();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       lrkv_bf16* orow = p.out + b * p.os_b + row * p.os_t + h * p.os_h;
@@ -502,6 +508,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     tc5::fence_after_sync();
     tc5::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Joins the splits' results: a warp per query row and head, four values to a lane.
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (i >= (long long)p.B * p.Hq * p.t_q) return;
+  const int row = (int)(i % p.t_q), h = (int)(i / p.t_q % p.Hq), b = (int)(i / p.t_q / p.Hq);
+  if (p.q_len && row >= p.q_len[b]) return;
+  const size_t step = (size_t)p.B * p.Hq * p.t_q * kPart;
+  const float* rec = p.part + (size_t)i * kPart;
+  float m = -INFINITY;
+  for (int s = 0; s < p.n_split; ++s) m = fmaxf(m, rec[s * step + kD]);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.n_split; ++s) {
+    const float* r = rec + s * step;
+    if (r[kD] == -INFINITY) continue;   // nothing was seen: its values were not written
+    const float w = ex2(r[kD] - m);
+    const float4 v = *reinterpret_cast<const float4*>(r + 4 * lane);
+    l = fmaf(w, r[kD + 1], l);
+    o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(p.out + b * p.os_b + row * p.os_t + h * p.os_h + 4 * lane) =
+      l > 0.f ? make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
 }
 
 }  // namespace prefill

@@ -5,6 +5,7 @@ Like the rest of the package it only marshals arguments and checks their shapes
 and types; the same names as in the C ABI are re-exported by the package.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass, fields
 
@@ -27,8 +28,9 @@ class _Score(ctypes.Structure):
 
 
 class _PrefillDims(ctypes.Structure):
+    # the strides one by one (q_stride[0] is q_stride0): making four arrays a call takes 2 us
     _fields_ = [(n, _I) for n in ("B", "Hq", "Hkv", "d", "t_q", "t_k")] + \
-        [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+        [(f"{n}_stride{i}", ctypes.c_int64) for n in ("q", "k", "v", "out") for i in range(3)]
 
 
 class _PagedDims(ctypes.Structure):
@@ -169,47 +171,57 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check(t, name, shape, dtype):
+def _check(t, name, shape, dtype, device=None):
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} is needed, got "
                          f"{t.dtype} {tuple(t.shape)}" + ("" if t.is_contiguous() else ", not contiguous"))
+    if device is not None and t.get_device() != device:
+        _wrong_device(t, name, device)
 
 
-def _check_score(score, B, t_q, Hq):
+def _wrong_device(t, name, device):
+    raise ValueError(f"{name}: a CUDA tensor on cuda:{device} is needed, got one on {t.device}")
+
+
+def _device(t, name):
+    """The device that the call's tensors have to be on: the library launches on the current one."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {t.device}")
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _check_score(score, B, t_q, Hq, device):
     if score is None or score._plain is not None:
         return
-    for name, shape, dtype in (("slopes", (Hq,), torch.float32), ("first_key", (B, t_q), torch.int32),
-                               ("prefix_end", (B, t_q), torch.int32)):
-        t = getattr(score, name)
-        if t is not None:
-            _check(t, name, shape, dtype)
-            _same_device(t, name)
+    if score.slopes is not None:
+        _check(score.slopes, "slopes", (Hq,), torch.float32, device)
+    if score.first_key is not None:
+        _check(score.first_key, "first_key", (B, t_q), torch.int32, device)
+    if score.prefix_end is not None:
+        _check(score.prefix_end, "prefix_end", (B, t_q), torch.int32, device)
 
 
-def _check_list(t, name, n):
+def _check_list(t, name, n, device):
     if t is not None:
-        _check(t, name, (n,), torch.int32)
-        _same_device(t, name)
+        _check(t, name, (n,), torch.int32, device)
 
 
-def _same_device(t, name):
-    # the library launches on the current device, whatever device the tensors are on
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {t.device}")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+def _check_ws(ws, device):
+    if ws is None:
+        return 0
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous uint8 tensor is needed")
+    if ws.get_device() != device:
+        _wrong_device(ws, "ws", device)
+    return ws.numel()
 
 
-def _check_ws(ws):
-    if ws is not None:
-        if ws.dtype != torch.uint8 or not ws.is_contiguous():
-            raise ValueError("ws: a contiguous uint8 tensor is needed")
-        _same_device(ws, "ws")
-
-
-def _stream(stream):
+def _stream(stream, device):
     # current_stream() builds an object (3 us); the raw handle is what the library takes
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _ref(score):
@@ -221,7 +233,6 @@ def _ref(score):
 def _cache_ref(dims, cache):
     if cache.dims is not dims and cache.dims != dims:
         raise ValueError(f"the cache was made for {cache.dims}, not {dims}")
-    _same_device(cache.k, "cache")
     return ctypes.byref(cache.c())
 
 
@@ -232,24 +243,24 @@ def _done(code, what, check):
     return code
 
 
-_Int64x3 = ctypes.c_int64 * 3
-
-
-def _strides(t):
-    a, b, c, _ = t.stride()
-    return _Int64x3(a, b, c)
-
-
 def _prefill_dims(q, k, v, out):
     B, t_q, Hq, d = q.shape
     _, t_k, Hkv, _ = k.shape
-    return _PrefillDims(B, Hq, Hkv, d, t_q, t_k, _strides(q), _strides(k), _strides(v), _strides(out))
+    return _PrefillDims(B, Hq, Hkv, d, t_q, t_k, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3])
 
 
-def _check_rows(t, name):
+@functools.lru_cache(maxsize=1024)
+def _prefill_ws(device, B, Hq, t_q, t_k):
+    """Bytes of workspace, which go by the sizes and the current device's SMs alone."""
+    dense = _PrefillDims(B, Hq, Hq, 128, t_q, t_k, *(4 * (max(t_q, t_k, 1) * Hq * 128, Hq * 128, 128)))
+    return load_serve_library().lrkv_prefill_workspace_size(ctypes.byref(dense))
+
+
+def _check_rows(t, name, device):
     if t.dtype != torch.bfloat16 or t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] > 1):
         raise ValueError(f"{name}: a bf16 tensor [B, t, heads, d] with contiguous rows is needed")
-    _same_device(t, name)
+    if t.get_device() != device:
+        _wrong_device(t, name, device)
 
 
 def lrkv_prefill_workspace_size(q, k, v, out):
@@ -261,28 +272,29 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
     """out [B,t_q,Hq,d] <- attention of q [B,t_q,Hq,d] over k, v [B,t_k,Hkv,d] (bf16, rows of d contiguous
     elements, otherwise any strides); see include/lrkv_serve.h.  A workspace is made when one is needed
     and none is given."""
-    _check_rows(q, "q")
-    _check_rows(k, "k")
-    _check_rows(v, "v")
-    _check_rows(out, "out")
+    device = _device(q, "q")
+    _check_rows(q, "q", device)
+    _check_rows(k, "k", device)
+    _check_rows(v, "v", device)
+    _check_rows(out, "out", device)
     B, t_q, Hq, d = q.shape
     if out.shape != q.shape or k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
         raise ValueError(f"shapes do not fit: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, "
                          f"out {tuple(out.shape)}")
-    _check_list(q_len, "q_len", B)
-    _check_list(kv_len, "kv_len", B)
-    _check_score(score, B, t_q, Hq)
-    if dev_status is not None:
-        _same_device(dev_status, "dev_status")
-    _check_ws(ws)
+    _check_list(q_len, "q_len", B, device)
+    _check_list(kv_len, "kv_len", B, device)
+    _check_score(score, B, t_q, Hq, device)
+    if dev_status is not None and dev_status.get_device() != device:
+        _wrong_device(dev_status, "dev_status", device)
+    n_ws = _check_ws(ws, device)
     lib, dims = load_serve_library(), ctypes.byref(_prefill_dims(q, k, v, out))
     if ws is None:
-        need = lib.lrkv_prefill_workspace_size(dims)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        n_ws = _prefill_ws(device, B, Hq, t_q, k.shape[1])
+        if n_ws:
+            ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
     return _done(lib.lrkv_prefill_attn(dims, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_len), _addr(kv_len),
-                                       _ref(score), out.data_ptr(), _addr(dev_status), _addr(ws),
-                                       0 if ws is None else ws.numel(), _stream(stream)), "lrkv_prefill_attn", check)
+                                       _ref(score), out.data_ptr(), _addr(dev_status), _addr(ws), n_ws,
+                                       _stream(stream, device)), "lrkv_prefill_attn", check)
 
 
 def lrkv_paged_workspace_size(dims, t_q=1):
@@ -300,91 +312,93 @@ def make_paged_workspace(dims, t_q=1, device="cuda"):
 def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=None, check=True):
     """Quantise k_new, v_new [B,t_new,Hkv,d] (bf16) into `layer`'s pages at positions seq_len .. ."""
     t_new = k_new.shape[1]
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _check(t, name, (dims.B, t_new, dims.Hkv, dims.d), torch.bfloat16)
-        _same_device(t, name)
-    _check_list(t_new_b, "t_new_b", dims.B)
+    shape = (dims.B, t_new, dims.Hkv, dims.d)
+    device = _device(cache.k, "cache")
+    _check(k_new, "k_new", shape, torch.bfloat16, device)
+    _check(v_new, "v_new", shape, torch.bfloat16, device)
+    _check_list(t_new_b, "t_new_b", dims.B, device)
     return _done(load_serve_library().lrkv_paged_append(
-        dims._ref, _cache_ref(dims, cache), layer, k_new.data_ptr(), v_new.data_ptr(), t_new,
-        _addr(t_new_b), _stream(stream)), "lrkv_paged_append", check)
+        dims._ref, _cache_ref(dims, cache), layer, k_new.data_ptr(), v_new.data_ptr(), t_new, _addr(t_new_b),
+        _stream(stream, device)), "lrkv_paged_append", check)
 
 
 def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None, check=True):
     """Positions first[b] .. first[b] + count[b] - 1 of `layer` as bf16 rows of k_out, v_out [B,t,Hkv,d]."""
     t_max = k_out.shape[1]
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _check(t, name, (dims.B, t_max, dims.Hkv, dims.d), torch.bfloat16)
-        _same_device(t, name)
-    _check_list(first, "first", dims.B)
-    _check_list(count, "count", dims.B)
+    shape = (dims.B, t_max, dims.Hkv, dims.d)
+    device = _device(cache.k, "cache")
+    _check(k_out, "k_out", shape, torch.bfloat16, device)
+    _check(v_out, "v_out", shape, torch.bfloat16, device)
+    _check_list(first, "first", dims.B, device)
+    _check_list(count, "count", dims.B, device)
     return _done(load_serve_library().lrkv_paged_read(
         dims._ref, _cache_ref(dims, cache), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
-        v_out.data_ptr(), _stream(stream)), "lrkv_paged_read", check)
+        v_out.data_ptr(), _stream(stream, device)), "lrkv_paged_read", check)
 
 
 def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None, stream=None, check=True):
     """out [B,t_q,Hq,d] <- attention of the newest t_q tokens' queries q (bf16) over `layer`'s pages."""
     t_q = q.shape[1]
-    for name, t in (("q", q), ("out", out)):
-        _check(t, name, (dims.B, t_q, dims.Hq, dims.d), torch.bfloat16)
-        _same_device(t, name)
-    _check_list(t_q_b, "t_q_b", dims.B)
-    _check_score(score, dims.B, t_q, dims.Hq)
-    _check_ws(ws)
+    shape = (dims.B, t_q, dims.Hq, dims.d)
+    device = _device(cache.k, "cache")
+    _check(q, "q", shape, torch.bfloat16, device)
+    _check(out, "out", shape, torch.bfloat16, device)
+    _check_list(t_q_b, "t_q_b", dims.B, device)
+    _check_score(score, dims.B, t_q, dims.Hq, device)
+    n_ws = _check_ws(ws, device)
     return _done(load_serve_library().lrkv_paged_attn(
-        dims._ref, _cache_ref(dims, cache), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score),
-        out.data_ptr(), _addr(ws), 0 if ws is None else ws.numel(), _stream(stream)), "lrkv_paged_attn", check)
+        dims._ref, _cache_ref(dims, cache), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score), out.data_ptr(),
+        _addr(ws), n_ws, _stream(stream, device)), "lrkv_paged_attn", check)
+
+
+def _count_call(fn, name, dims, cache, t_new, t_new_b, stream, check):
+    device = _device(cache.k, "cache")
+    _check_list(t_new_b, "t_new_b", dims.B, device)
+    return _done(fn(dims._ref, _cache_ref(dims, cache), t_new, _addr(t_new_b), _stream(stream, device)), name, check)
 
 
 def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """Pages for t_new (or t_new_b[b]) more tokens of every sequence."""
-    _check_list(t_new_b, "t_new_b", dims.B)
-    return _done(load_serve_library().lrkv_pages_reserve(dims._ref, _cache_ref(dims, cache), t_new,
-                                                         _addr(t_new_b), _stream(stream)), "lrkv_pages_reserve", check)
+    return _count_call(load_serve_library().lrkv_pages_reserve, "lrkv_pages_reserve", dims, cache, t_new, t_new_b,
+                       stream, check)
 
 
 def lrkv_pages_advance(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """seq_len += t_new (or t_new_b)."""
-    _check_list(t_new_b, "t_new_b", dims.B)
-    return _done(load_serve_library().lrkv_pages_advance(dims._ref, _cache_ref(dims, cache), t_new,
-                                                         _addr(t_new_b), _stream(stream)), "lrkv_pages_advance", check)
+    return _count_call(load_serve_library().lrkv_pages_advance, "lrkv_pages_advance", dims, cache, t_new, t_new_b,
+                       stream, check)
 
 
-def _pair(src, dst):
-    _check_list(src, "src", src.numel())
-    _check_list(dst, "dst", src.numel())
-    return src.data_ptr(), dst.data_ptr(), src.numel()
+def _pair_call(fn, name, dims, cache, src, dst, ws, stream, check):
+    device, n = _device(cache.k, "cache"), src.numel()
+    _check_list(src, "src", n, device)
+    _check_list(dst, "dst", n, device)
+    n_ws = _check_ws(ws, device)
+    return _done(fn(dims._ref, _cache_ref(dims, cache), src.data_ptr(), dst.data_ptr(), n, _addr(ws), n_ws,
+                    _stream(stream, device)), name, check)
 
 
 def lrkv_pages_fork(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Sequence dst[i] becomes a copy of sequence src[i] (int32 lists on the device)."""
-    s, d, n = _pair(src, dst)
-    _check_ws(ws)
-    return _done(load_serve_library().lrkv_pages_fork(
-        dims._ref, _cache_ref(dims, cache), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
-        _stream(stream)), "lrkv_pages_fork", check)
-
-
-def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
-    """Empty the sequences listed in seqs (int32, on the device)."""
-    _check_list(seqs, "seqs", seqs.numel())
-    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache),
-                                                      seqs.data_ptr(), seqs.numel(), _stream(stream)),
-                 "lrkv_pages_free", check)
+    return _pair_call(load_serve_library().lrkv_pages_fork, "lrkv_pages_fork", dims, cache, src, dst, ws, stream, check)
 
 
 def lrkv_pages_copy(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Copy pages src[i] to dst[i] (int32 lists on the device) in every layer."""
-    s, d, n = _pair(src, dst)
-    _check_ws(ws)
-    return _done(load_serve_library().lrkv_pages_copy(
-        dims._ref, _cache_ref(dims, cache), s, d, n, _addr(ws), 0 if ws is None else ws.numel(),
-        _stream(stream)), "lrkv_pages_copy", check)
+    return _pair_call(load_serve_library().lrkv_pages_copy, "lrkv_pages_copy", dims, cache, src, dst, ws, stream, check)
+
+
+def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
+    """Empty the sequences listed in seqs (int32, on the device)."""
+    device, n = _device(cache.k, "cache"), seqs.numel()
+    _check_list(seqs, "seqs", n, device)
+    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache), seqs.data_ptr(), n,
+                                                      _stream(stream, device)), "lrkv_pages_free", check)
 
 
 def lrkv_pages_compact(dims, cache, ws=None, stream=None, check=True):
     """Move pages so that the live ones have the lowest ids."""
-    _check_ws(ws)
-    return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache), _addr(ws),
-                                                         0 if ws is None else ws.numel(), _stream(stream)),
-                 "lrkv_pages_compact", check)
+    device = _device(cache.k, "cache")
+    n_ws = _check_ws(ws, device)
+    return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache), _addr(ws), n_ws,
+                                                         _stream(stream, device)), "lrkv_pages_compact", check)

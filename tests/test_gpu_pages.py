@@ -301,3 +301,27 @@ def test_a_serving_run(code):
     for h in range(Hq):
         U.check_rows(out[1, :, h], q[1, :, h], kk[1, :, h // 4], vv[1, :, h // 4], pos, old + new, score, h, 0, U.U)
     assert int(c.dev_status[0]) == 0
+
+
+def test_binding_refuses_tensors_that_do_not_fit():
+    D, c, ws = filled(2, 16, 4, 2)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")
+    other = L.PagedDims(B=2, Hq=4, Hkv=2, d=128, page=32, n_pages=4, max_pages=2, n_layers=2)
+    with pytest.raises(ValueError, match="shape"):
+        L.lrkv_paged_append(D, c, 0, bf(2, 1, 4, 128), bf(2, 1, 4, 128))
+    with pytest.raises(ValueError, match="made for"):
+        L.lrkv_pages_reserve(other, c, 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.lrkv_pages_free(D, c, torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="uint8"):
+        L.lrkv_pages_compact(D, c, ws=ws.view(torch.int32))
+    with pytest.raises(ValueError, match="dst"):
+        L.lrkv_pages_copy(D, c, U.ints([0, 1]), U.ints([2]), ws=ws)
+    with pytest.raises(ValueError, match="slopes"):
+        L.lrkv_paged_attn(D, c, 0, bf(2, 1, 4, 128), bf(2, 1, 4, 128), score=L.Score(slopes=U.slopes(3)), ws=ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.lrkv_prefill_attn(bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128).cpu(), bf(1, 4, 4, 128))
+    with pytest.raises(L.LrkvError):
+        L.lrkv_paged_attn(D, c, 2, bf(2, 1, 4, 128), bf(2, 1, 4, 128), ws=ws)
+    with pytest.raises(L.LrkvError):
+        L.lrkv_pages_compact(D, c)

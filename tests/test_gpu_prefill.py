@@ -223,3 +223,36 @@ def test_long_prompts(t_q, t_k):
     q, k, v = inputs(1, 4, 1, t_q, t_k)
     out, _ = run(q, k, v)
     check(out, q, k, v)
+
+
+@pytest.mark.parametrize("score", [dict(), dict(window=700), dict(docs=True, softcap=20.0), dict(prefix=True, bias=True)],
+                         ids=str)
+def test_keys_split_over_ctas(score):
+    """Few rows after many keys: the keys of a row block are shared out, also where a share is empty."""
+    t_q, t_k = 70, 6000
+    q, k, v = inputs(2, 4, 2, t_q, t_k)
+    s = dict(score)
+    first = None
+    if s.pop("docs", False):
+        first = doc_starts(2, t_q, [5950, 5990], t_k - t_q)
+        first[0, :30], first[1, 10] = 100, 10 ** 7
+    end = torch.full((2, t_q), 5980, dtype=torch.int32, device="cuda") if s.pop("prefix", False) else None
+    s = L.Score(slopes=U.slopes(4) if s.pop("bias", False) else None, first_key=first, prefix_end=end, **s)
+    out = torch.full_like(q, CANARY)
+    need = L.lrkv_prefill_workspace_size(q, k, v, out)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")     # any contents: here NaN
+    args = dict(q_len=[t_q, 33], kv_len=[t_k, 5000], score=s)
+    run(q, k, v, out=out, ws=ws, **args)
+    check(out, q, k, v, **args)
+    if first is not None:
+        assert bool((run(q, k, v, score=s)[0][1, 10] == 0).all())
+    with pytest.raises(L.LrkvError):
+        run(q, k, v, ws=ws[:need - 16])
+    again = torch.full_like(q, CANARY)
+    lens = {n: U.ints(args[n]) for n in ("q_len", "kv_len")}
+    g = U.graph_of(lambda: L.lrkv_prefill_attn(q, k, v, again, score=s, ws=ws, **lens))
+    again.fill_(CANARY)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)

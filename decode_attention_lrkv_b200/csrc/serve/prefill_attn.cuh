@@ -30,8 +30,8 @@
 // 10 clocks of work on the fp32 pipe against 8 on the special-function unit, no faster.
 //
 // The running reference m only moves when a row's maximum passes it by more than
-// 2^8 (weights then stay below 2^8, and the row's sum is in fp32): O is rescaled
-// in tensor memory a few times per row instead of once per unit.  The group that does
+// 2^24 (bf16 and fp32 weights up to 2^24 are as exact as others): O is rescaled in tensor
+// memory once or never per row instead of once per unit.  The group that does
 // it first waits for the scores of the next unit: MMAs complete in order, so the last
 // product into O is complete, and the next one waits for this group's P.
 //
@@ -63,7 +63,7 @@ constexpr int kUnitBox = kUnitBytes / 2;
 constexpr int kKStages = 4, kVStages = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 X (+ 64 (unit & 1) for S)
-constexpr float kLazy = 8.f;                // rescale when a maximum grows by more (log2)
+constexpr float kLazy = 24.f;               // rescale when a maximum grows by more (log2)
 
 // Shared memory: Q blocks, key ring, value ring (each 1024-aligned), barriers.
 constexpr int kOffQ = 0;
@@ -242,17 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (t0[x] >= t1[x]) t0[x] = 0x7ffffff0, t1[x] = 0;
     }
   }
-  // With a distance bias the units are taken from the last one down, the nearest keys first:
-  // a row then has its maximum at once.  Upwards the reference of a steep head moves in every
-  // unit (32 heads, bias over 16384 keys: 2270 us upwards, 1790 down).  Without a bias upwards is
-  // better: under a causal mask the last units hold a single key for some rows, and more
-  // references move later (8192 tokens: 544 us upwards, 565 down).  From here on units are
-  // numbered in the order they are taken.
+  // The units are taken from the last one down, the nearest keys first: with a distance bias a
+  // row then has its maximum at once.  Upwards the reference of a steep head moves in every unit
+  // (32 heads, bias over 16384 keys: 2212 us upwards, 1750 down).  From here on units are numbered
+  // in the order they are taken.
   const int j0 = min(t0[0], t0[1]), j1 = max(t1[0], t1[1]), top = j0 + j1 - 1;
-  auto first_key_of = [&](int j) { return (BIAS ? top - j : j) * kUnit; };
+  auto first_key_of = [&](int j) { return (top - j) * kUnit; };
 #pragma unroll
   for (int x = 0; x < 2; ++x)
-    if (BIAS && t0[x] < t1[x]) {
+    if (t0[x] < t1[x]) {
       const int last = t1[x] - 1;
       t1[x] = top - t0[x] + 1;
       t0[x] = top - last;

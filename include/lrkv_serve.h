@@ -82,7 +82,8 @@ typedef struct {
  *   be finite (a hidden key's value enters with weight zero).
  * out must not overlap q, k or v.
  * Scores and the softmax are in fp32; the weights are rounded to bf16 for the
- *   product with v, as v is bf16 (the sum that divides them is not).
+ *   product with v, as v is bf16 (the sum that divides them is not).  Sums run up to
+ *   2^24 times the weights' total: values have to stay below 2^80.
  * dev_status: nullable, 1 word of LRKV_DEV_* bits.
  * ws: lrkv_prefill_workspace_size(dims) bytes, any contents (0 bytes: may be
  *   null).  When there are few query rows the keys of a row block are split

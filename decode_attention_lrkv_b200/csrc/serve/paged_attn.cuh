@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     const int h = p.row_blocks == 1 ? at.hr : at.hr / p.row_blocks, rb = at.hr - h * p.row_blocks;
     const int n_tiles = min(at.s.tiles - at.tile, end - x);
     const int rho0 = rb * p.per_block, rho1 = min(min(rho0 + p.per_block, p.g * p.t_q), p.g * at.s.n_rows);
-    uint2 q_first[8];
+    uint2 q_next[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) q_first[c] = make_uint2(0u, 0u);
-    load_q(at, rho0 + g8, rho1, h, q_first);
+    for (int c = 0; c < 8; ++c) q_next[c] = make_uint2(0u, 0u);
+    load_q(at, rho0 + g8, rho1, h, q_next);
     if (first) {   // beside the queries' way
       prod.at = at;
       prod.load_rows(p, lane);
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     for (int nb = 0; nb < NB; ++nb) {
       uint2 w[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = nb == 0 ? q_first[c] : make_uint2(0u, 0u);
-      if (nb > 0) load_q(at, rho0 + 8 * nb + g8, rho1, h, w);
+      for (int c = 0; c < 8; ++c) w[c] = q_next[c], q_next[c] = make_uint2(0u, 0u);
+      if (nb + 1 < NB) load_q(at, rho0 + 8 * (nb + 1) + g8, rho1, h, q_next);
       uint32_t mag = 0;
 #pragma unroll
       for (int c = 0; c < 8; ++c) mag = __vmaxu2(mag, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu));

@@ -106,6 +106,24 @@ def test_ragged_batches_split_over_many_ctas(page, code):
     assert torch.equal(attn(D, c, q, ws=ws), first)         # the workspace is as it was, the result the same
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("Hq,Hkv,t_q", [(8, 2, 3), (8, 2, 4), (4, 1, 5), (8, 1, 4), (8, 1, 9)])
+def test_rows_of_a_cache_larger_than_l2(Hq, Hkv, t_q, page, code):
+    """12 to 72 rows of a kv head, in blocks of up to 32: the table has room for a long context."""
+    lens = [900, 2, 0, 333]
+    D, c = make(4, Hq, Hkv, page, lens, code, room=t_q)
+    wide = L.PagedDims(B=4, Hq=Hq, Hkv=Hkv, d=128, page=page, n_pages=D.n_pages, max_pages=8000000 // page, code=code)
+    table = torch.full((4, wide.max_pages), -1, dtype=torch.int32, device="cuda")
+    table[:, :D.max_pages] = c.page_table
+    w = L.PagedCache(wide, k=c.k, v=c.v, scale_k=c.scale_k, scale_v=c.scale_v, refs=c.refs, seq_len=c.seq_len,
+                     page_table=table)
+    q = U.normal(4, 4, t_q, Hq, 128, std=2.0)
+    for s in (L.Score(), L.Score(window=250, slopes=U.slopes(Hq), softcap=30.0)):
+        some = [t_q, t_q, t_q - 1, 0]
+        check(attn(wide, w, q, some, s), D, c, q, some, s)
+
+
 def test_long_context():
     D, c = make(1, 4, 1, 128, [70000], "int8")
     q = U.normal(6, 1, 1, 4, 128, std=2.0)

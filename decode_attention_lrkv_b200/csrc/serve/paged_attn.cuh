@@ -8,7 +8,7 @@
 // (sequence, kv head, block of up to 24 query rows) are cut into tiles of 32 tokens
 // and numbered; every warp of the grid takes an equal, contiguous run of tiles, so
 // ragged lengths, few long sequences and many short ones all fill the SMs alike.
-// A warp works alone: its lane 0 brings tiles in by TMA (128-byte swizzle, a ring of
+// A warp works alone: one thread of it brings tiles in by TMA (128-byte swizzle, a ring of
 // kStages tiles of keys and values, the scales by 4-byte copies on the same barrier),
 // and the warp multiplies with mma.sync m16n8k16, f16 operands, fp32 sums:
 //     S^T = K Q^T   (A: 16 tokens x 16 dims of codes; B: 8 query rows)
@@ -294,7 +294,7 @@ struct Producer {
       a = __shfl_sync(0xffffffffu, row_a, at.tile - rows_at);
       b = PT == 16 ? __shfl_sync(0xffffffffu, row_b, at.tile - rows_at) : kNotNeeded;
     }
-    if (lane == 0) {
+    if (elect_one()) {
       unsigned char* dst = ring + slot * kUnitBytes;
       uint64_t* bar = &sh.bars[warp][slot];
       float* sc = sh.scale[warp][slot];

@@ -5,11 +5,11 @@
 // and the scale s of the page that j lies on.
 //
 // Bound: memory (2 d bytes a token and kv head, read once).  The keys of all
-// (sequence, kv head, block of up to 24 query rows) are cut into tiles of 32 tokens
+// (sequence, kv head, block of up to 32 query rows) are cut into tiles of 32 tokens
 // and numbered; every warp of the grid takes an equal, contiguous run of tiles, so
 // ragged lengths, few long sequences and many short ones all fill the SMs alike.
 // A warp works alone: one thread of it brings tiles in by TMA (128-byte swizzle, a ring of
-// kStages tiles of keys and values, the scales by 4-byte copies on the same barrier),
+// units, tiles of keys and of values in turn, the scales by 4-byte copies on the same barrier),
 // and the warp multiplies with mma.sync m16n8k16, f16 operands, fp32 sums:
 //     S^T = K Q^T   (A: 16 tokens x 16 dims of codes; B: 8 query rows)
 //     O^T = V^T P^T (A: 16 dims x 16 tokens of codes; B: weights)
@@ -36,7 +36,6 @@ namespace paged {
 constexpr int kTile = 32;                // tokens
 constexpr int kUnitBytes = kTile * kD;   // codes of a tile's keys, or of its values
 constexpr float kLazyMax = 8.f;          // rescale when a maximum grows by more (log2)
-constexpr float kShift = 1152.f;         // what is added to an int8 code when it becomes f16
 
 struct AttnParams {
   CUtensorMap map_k, map_v;   // codes as rows of 128 bytes; box {128, min(page, 32)}
@@ -91,7 +90,7 @@ struct AttnConfig {
     Piece open[2];                          // segments shared with other CTAs: with earlier ones, with later ones alone
     int prefix[kThreads + 1];               // tiles of one kv head before every group of sequences
     int warp_sum[kWarps];
-    int abort, last[2];
+    int abort, last[2], first_cta[2], ctas[2];   // of the open segments
   };
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + sizeof(Shared) + 1024;
 };
@@ -218,11 +217,12 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Codes to f16x2 of the word's bytes (0, 1) and (2, 3), exactly; int8 codes with kShift
+// Codes to f16x2 of the word's bytes (0, 1) and (2, 3), exactly; int8 codes with 1152
 // added: a byte with its sign bit flipped is code + 128, and the f16 with high byte 0x64
 // and that low byte is 1024 more.  The sums that such operands enter start from what the
 // shift adds to them, with the sign turned.  (Taking the shift off every operand instead,
-// by two more instructions per word: 205 against 193 us at 131072 tokens x 32 heads.)
+// by two more instructions per word: 168 against 164 us at 131072 tokens x 32 heads, 182 against
+// 174 under the power limit; 89 against 81 us for sixteen sequences of 8K to 16K x 8 heads.)
 template <int CODE>
 __device__ __forceinline__ void codes_pairs(uint32_t w, uint32_t& h01, uint32_t& h23) {
   if (CODE == LRKV_CODE_INT8) {
@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
   if (tid == 0) {
     sh.abort = 0;
     sh.open[0].seg = sh.open[1].seg = -1;
+    sh.last[0] = sh.last[1] = 0;
     tc5::prefetch_tensormap(&p.map_k);
     tc5::prefetch_tensormap(&p.map_v);
   }
@@ -850,81 +851,62 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
   __syncthreads();
   if (sh.abort && tid == 0) atomicOr(p.C.dev_status, LRKV_DEV_WAIT_TIMEOUT);
 
-  // query rows of a piece's sequence, and the first of its block
-  auto piece_rows = [&](const Piece& pc, int* rho0, int* h) {
-    uint32_t st = 0;
-    *h = pc.hr / p.row_blocks;
-    *rho0 = pc.hr % p.row_blocks * p.per_block;
-    return min(min(*rho0 + p.per_block, p.g * p.t_q), p.g * call_tokens(p.t_q_b, pc.b, p.t_q, &st));
-  };
   const int X0 = workers.start(blockIdx.x * W), X1 = workers.start((blockIdx.x + 1) * W);
-  // join the pieces of a segment: the warps that hold them share the rows
-  for (int k = 0; k < 2; ++k) {
-    const Piece mine = sh.piece[warp][k];
-    if (mine.seg < 0) continue;
-    const int seg = lane < 2 * W ? sh.piece[lane >> 1][lane & 1].seg : -1;
-    const uint32_t members = __ballot_sync(0xffffffffu, seg == mine.seg);
-    const int n = __popc(members), rank = __popc(members & ((1u << (2 * warp + k)) - 1u));
-    const int place = nth_bit(members, min(lane, n - 1)), w = place >> 1;
-    const float* rec = place & 1 ? reinterpret_cast<const float*>(sm + w * C::kWarpBytes)
-                                 : p.recs + ((size_t)blockIdx.x * (2 + W) + 2 + w) * kRec;
-    int rho0, h;
-    const int rho1 = piece_rows(mine, &rho0, &h);
-    const bool done = mine.seg >= X0 && mine.seg + mine.tiles <= X1;
-    const int which = mine.seg >= X0 ? 1 : 0;
-    float* dst = p.recs + ((size_t)blockIdx.x * (2 + W) + which) * kRec;
-    for (int row0 = rank; rho0 + row0 < rho1; row0 += kJoin * n) {
-      float4 o[kJoin];
-      float m[kJoin], l[kJoin];
-      join_rows(n, rec, ROWS, row0, n, rho1 - rho0, lane, o, m, l);
-#pragma unroll
-      for (int j = 0; j < kJoin; ++j) {
-        const int row = row0 + j * n;
-        if (rho0 + row >= rho1) continue;
-        if (done) {
-          store_row4(p.out + row_offset(p, mine.b, h, rho0 + row) + 4 * lane, o[j], l[j]);
-        } else {
-          *reinterpret_cast<float4*>(dst + row * kRecRow + 4 * lane) = o[j];
-          if (lane == 0) dst[ROWS * kRecRow + row] = m[j], dst[ROWS * kRecRow + ROWS + row] = l[j];
-        }
-      }
-    }
-    if (!done && rank == 0 && lane == 0) sh.open[which] = mine;
-  }
-  __syncthreads();
-  Piece shared_piece[2] = {sh.open[0], sh.open[1]};
-  if (shared_piece[0].seg < 0 && shared_piece[1].seg < 0) return;
   auto cta_of = [&](int tile) { return workers.of(tile) / W; };
-  if (tid == 0) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sh.last[k] = 0;
-      if (shared_piece[k].seg < 0) continue;
-      const int c0 = cta_of(shared_piece[k].seg), c1 = cta_of(shared_piece[k].seg + shared_piece[k].tiles - 1);
-      if (atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0) {
-        p.tickets[c0] = 0;
-        sh.last[k] = 1;
+  // Rounds 0 and 1 join the pieces of a segment that lie in this CTA: the warps that hold them
+  // share the rows.  Rounds 2 and 3 join the records of a segment that several CTAs share, where
+  // this CTA is the last to arrive: with earlier CTAs, with later ones.  (One copy of the code for
+  // all rounds: much of a short call's time goes on fetching instructions for the first time.)
+#pragma unroll 1
+  for (int round = 0; round < 4; ++round) {
+    if (round == 2) {
+      __syncthreads();
+      if (sh.open[0].seg < 0 && sh.open[1].seg < 0) return;
+      if (tid < 2 && sh.open[tid].seg >= 0) {
+        const int c0 = cta_of(sh.open[tid].seg), c1 = cta_of(sh.open[tid].seg + sh.open[tid].tiles - 1);
+        sh.last[tid] = atom_add_acq_rel_gpu(p.tickets + c0, 1) == c1 - c0;
+        if (sh.last[tid]) p.tickets[c0] = 0;
+        sh.first_cta[tid] = c0;
+        sh.ctas[tid] = c1 - c0 + 1;
       }
+      __syncthreads();
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (shared_piece[k].seg < 0 || !sh.last[k]) continue;
-    const Piece first = shared_piece[k];
-    const int c0 = cta_of(first.seg), c1 = cta_of(first.seg + first.tiles - 1);
-    int rho0, h;
-    const int rho1 = piece_rows(first, &rho0, &h);
-    const int n = c1 - c0 + 1;
-    for (int row0 = warp; rho0 + row0 < rho1; row0 += kJoin * W) {
+    const bool mine = round < 2;
+    const Piece pc = mine ? sh.piece[warp][round] : sh.open[round - 2];
+    if (pc.seg < 0 || (!mine && !sh.last[round - 2])) continue;
+    // query rows of the block
+    uint32_t st = 0;
+    const int h = p.row_blocks == 1 ? pc.hr : pc.hr / p.row_blocks, rho0 = (pc.hr - h * p.row_blocks) * p.per_block;
+    const int rows = min(min(p.per_block, p.g * p.t_q - rho0), p.g * call_tokens(p.t_q_b, pc.b, p.t_q, &st) - rho0);
+    int n, row0 = warp, step = W;
+    const float* rec = nullptr;
+    const bool done = !mine || (pc.seg >= X0 && pc.seg + pc.tiles <= X1);
+    const int which = pc.seg >= X0 ? 1 : 0;
+    float* dst = p.recs + ((size_t)blockIdx.x * (2 + W) + which) * kRec;
+    if (mine) {
+      const int seg = lane < 2 * W ? sh.piece[lane >> 1][lane & 1].seg : -1;
+      const uint32_t members = __ballot_sync(0xffffffffu, seg == pc.seg);
+      step = n = __popc(members);
+      row0 = __popc(members & ((1u << (2 * warp + round)) - 1u));
+      const int place = nth_bit(members, min(lane, n - 1)), w = place >> 1;
+      rec = place & 1 ? reinterpret_cast<const float*>(sm + w * C::kWarpBytes)
+                      : p.recs + ((size_t)blockIdx.x * (2 + W) + 2 + w) * kRec;
+      if (!done && row0 == 0 && lane == 0) sh.open[which] = pc;
+    } else {
+      n = sh.ctas[round - 2];
+    }
+    for (; row0 < rows; row0 += kJoin * step) {
       float4 o[kJoin];
       float m[kJoin], l[kJoin];
+#pragma unroll 1
       for (int i0 = 0; i0 < n; i0 += 32) {   // up to 32 records at a time
+        if (!mine) {
+          const int i = min(i0 + lane, n - 1);
+          rec = p.recs + ((size_t)(sh.first_cta[round - 2] + i) * (2 + W) + (i == 0 ? 1 : 0)) * kRec;
+        }
         float4 o1[kJoin];
         float m1[kJoin], l1[kJoin];
-        const int i = min(i0 + lane, n - 1);
-        const float* rec = p.recs + ((size_t)(c0 + i) * (2 + W) + (i == 0 ? 1 : 0)) * kRec;
-        join_rows(min(32, n - i0), rec, ROWS, row0, W, rho1 - rho0, lane, o1, m1, l1);
+        join_rows<kJoin>(min(32, n - i0), rec, ROWS, row0, step, rows, lane, o1, m1, l1);
 #pragma unroll
         for (int j = 0; j < kJoin; ++j) {
           if (i0 == 0) {
@@ -940,9 +922,16 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
         }
       }
 #pragma unroll
-      for (int j = 0; j < kJoin; ++j)
-        if (rho0 + row0 + j * W < rho1)
-          store_row4(p.out + row_offset(p, first.b, h, rho0 + row0 + j * W) + 4 * lane, o[j], l[j]);
+      for (int j = 0; j < kJoin; ++j) {
+        const int row = row0 + j * step;
+        if (row >= rows) continue;
+        if (done) {
+          store_row4(p.out + row_offset(p, pc.b, h, rho0 + row) + 4 * lane, o[j], l[j]);
+        } else {
+          *reinterpret_cast<float4*>(dst + row * kRecRow + 4 * lane) = o[j];
+          if (lane == 0) dst[ROWS * kRecRow + row] = m[j], dst[ROWS * kRecRow + ROWS + row] = l[j];
+        }
+      }
     }
   }
 }

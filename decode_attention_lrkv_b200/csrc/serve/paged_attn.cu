@@ -73,7 +73,8 @@ lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   p.window = sc.window;
   p.row_log2 = sc.scale * kLog2e;
   if (sc.softcap > 0.f) {
-    p.cap_in = 2.f / sc.softcap;
+    p.cap_unit = 1.f / (sc.softcap * kLog2e);
+    serve::cap_polynomial(sc.softcap, p.cap_poly);
     p.cap_log2 = sc.softcap * kLog2e;
   }
   unsigned char* base = static_cast<unsigned char*>(ws);

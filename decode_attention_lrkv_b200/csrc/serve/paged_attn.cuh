@@ -55,7 +55,8 @@ struct AttnParams {
   int hr_shift;
   uint32_t g_mul;    // numbers below 2^10 divided by g: x g_mul >> 16
   float row_log2;    // scale * log2(e)
-  float cap_in;      // 2 / softcap: exponent of e in tanh, per unit of a score (0: no cap)
+  float cap_unit;    // 1 / (softcap log2(e)): a score in log2 units as tanh's argument (0: no cap)
+  float cap_poly[6]; // softcap log2(e) tanh(x) = x (cap_poly[0] + cap_poly[1] x^2 + ..), |x| <= 1
   float cap_log2;    // softcap * log2(e)
 };
 
@@ -680,14 +681,21 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           f[nb][0][j] = fmaxf(sk0 * row.mul[j], FLT_MIN);   // not 0: an unseen key stays at -inf
           if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = fmaxf(sk1 * row.mul[j], FLT_MIN);
         }
-        if (p.cap_in > 0.f || p.slopes) {
+        if (p.cap_unit > 0.f || p.slopes) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float v = s[nb][mt][k] * f[nb][PT == 16 ? mt : 0][k & 1];
-              if (p.cap_in > 0.f)   // softcap tanh(x / softcap) = softcap (1 - 2 / (1 + e^(2 x / softcap)))
-                v = fmaf(-2.f * p.cap_log2, rcp_fast(1.f + ex2(v * p.cap_in)), p.cap_log2);
+              if (p.cap_unit > 0.f) {
+                const float x = v * p.cap_unit, t = x * x;
+                float r = p.cap_poly[5];
+#pragma unroll
+                for (int i = 4; i >= 0; --i) r = fmaf(r, t, p.cap_poly[i]);
+                v = x * r;
+                if (fabsf(x) > 1.f)   // tanh x = 1 - 2 / (1 + e^(2 x)), which cancels near 0
+                  v = fmaf(-2.f * p.cap_log2, rcp_fast(1.f + ex2(x * (2.f * kLog2e))), p.cap_log2);
+              }
               if (p.slopes) {       // positions are below 2^24: exact in fp32
                 const float dist = (float)(base + g8 + mt * 16 + 8 * (k >> 1)) - row.pos[k & 1];
                 v = fmaf(-row.slope[k & 1], fabsf(dist), v);

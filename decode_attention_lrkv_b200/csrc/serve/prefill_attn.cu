@@ -118,8 +118,7 @@ lrkv_status lrkv_prefill_attn(const lrkv_prefill_dims* dims, const lrkv_bf16* q,
   p.qk_log2 = sc.scale * kLog2e;
   const bool cap = sc.softcap > 0.f, bias = sc.slopes != nullptr;
   if (cap) {
-    constexpr float kTanh[6] = {0.9999994f, -0.33329043f, 0.13281433f, -0.051605646f, 0.016743084f, -0.0030670483f};
-    for (int i = 0; i < 6; ++i) p.cap_poly[i] = sc.softcap * kLog2e * kTanh[i];
+    serve::cap_polynomial(sc.softcap, p.cap_poly);
     p.cap_unit = sc.scale / sc.softcap;
     p.cap_in = 2.f * kLog2e * sc.scale / sc.softcap;
     p.cap_log2 = sc.softcap * kLog2e;

@@ -110,8 +110,7 @@ static_assert(sizeof(Bars) <= 256, "barrier region");
 
 // s[c] = softcap log2(e) tanh(scale s[c] / softcap).  Where all |x| = |scale s / softcap| of
 // the warp are at most 1, as sane logits are, by a polynomial in x^2 on the two-wide fp32
-// pipe (a least-squares fit of tanh(x) / x, weighted towards equal relative errors: 6.5e-7
-// at most with fp32 rounding, 4e-5 in the exponent at softcap 50); else by
+// pipe (relative error 6.5e-7: at most 4e-5 in the exponent at softcap 50); else by
 // tanh(x) = 1 - 2 / (1 + e^(2x)), two special-function results for each score.
 __device__ __forceinline__ void cap_scores(const Params& p, float (&s)[kUnit]) {
   float top0 = 0.f, top1 = 0.f;

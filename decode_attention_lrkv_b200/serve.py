@@ -221,7 +221,11 @@ def _check_ws(ws, device):
 
 def _stream(stream, device):
     # current_stream() builds an object (3 us); the raw handle is what the library takes
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"stream is one of cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _ref(score):
@@ -290,8 +294,9 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
     lib, dims = load_serve_library(), ctypes.byref(_prefill_dims(q, k, v, out))
     if ws is None:
         n_ws = _prefill_ws(device, B, Hq, t_q, k.shape[1])
-        if n_ws:
-            ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
+        if n_ws:   # memory of the stream that uses it: it may be handed on as soon as this call returns
+            with torch.cuda.stream(stream):
+                ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device)
     return _done(lib.lrkv_prefill_attn(dims, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_len), _addr(kv_len),
                                        _ref(score), out.data_ptr(), _addr(dev_status), _addr(ws), n_ws,
                                        _stream(stream, device)), "lrkv_prefill_attn", check)

@@ -8,7 +8,8 @@ weights.  An output differs from o by at most
   the end   one rounding to bf16: u |o|.
 A score's error: an fp32 sum of 128 products, at most 128 2^-24 sum|q k| scale (a factor of
 2 for the tensor core's own order), the factors, tanh and exponential in fp32: 2^-20 of the
-score's size, and for a tanh cap 2e-6 of the cap.
+score's size, and for a tanh cap 2e-6 of the cap or, where every score is small against it,
+of four times the largest one.
 """
 import torch
 
@@ -27,7 +28,7 @@ def close(got, ref, rows_err):
 
 
 def score_error(ref, softcap):
-    return 2 * 128 * 2.0 ** -24 * ref[4] + 2.0 ** -20 * (ref[3] + 1) + (2e-6 * softcap if softcap else 0.0)
+    return 2 * 128 * 2.0 ** -24 * ref[4] + 2.0 ** -20 * (ref[3] + 1) + (2e-6 * (4 * ref[3]).clamp_max(softcap) if softcap else 0.0)
 
 
 def check_rows(got, q, k, v, pos, total, score, h, b, w, floor=0.0, extra_score=0.0):

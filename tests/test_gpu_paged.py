@@ -147,7 +147,7 @@ def test_many_short_sequences():
 
 
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
-@pytest.mark.parametrize("score", [dict(softcap=20.0), dict(softcap=2.0), dict(window=1), dict(window=33), dict(window=500),
+@pytest.mark.parametrize("score", [dict(softcap=20.0), dict(softcap=2.0), dict(softcap=1e5), dict(window=1), dict(window=33), dict(window=500),
                                    dict(scale=0.3), dict(bias=True), dict(bias=True, softcap=30.0, window=700)], ids=str)
 def test_score_modifiers(score, code):
     score = dict(score)

@@ -82,7 +82,7 @@ def test_no_keys_and_counts_out_of_range():
     run(empty, k[:2], v[:2])                                # no rows: nothing happens
 
 
-@pytest.mark.parametrize("softcap,std", [(20.0, 2.0), (50.0, 2.0), (5.0, 6.0), (1.0, 30.0), (2000.0, 2.0)])
+@pytest.mark.parametrize("softcap,std", [(20.0, 2.0), (50.0, 2.0), (5.0, 6.0), (1.0, 30.0), (2000.0, 2.0), (1e6, 2.0)])
 def test_tanh_cap(softcap, std):
     """Small and large scores take the polynomial and the exponential form."""
     q, k, v = inputs(1, 4, 2, 200, 400, std=std)

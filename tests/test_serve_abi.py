@@ -57,7 +57,8 @@ def test_prefill_refusals(lib):
     for bad in ("q", "k", "v", "out", "q_len", "kv_len"):
         assert _prefill(lib, **{bad: FAKE + 8}) == ALIGN, bad
     for bad in (dict(scale=-1.0), dict(scale=float("nan")), dict(softcap=-2.0), dict(softcap=float("inf")),
-                dict(softcap=1e-35), dict(window=-1)):
+                dict(softcap=1e-35), dict(window=-1),
+                dict(scale=1e10, softcap=1e-25)):
         assert _prefill(lib, score=S._Score(**bad)) == INVALID, bad
     assert _prefill(lib, score=S._Score(slopes=FAKE + 4)) == ALIGN
     assert _prefill(lib, t_q=0) == 0                       # no rows: nothing to do

@@ -22,14 +22,18 @@ bool codes_map(CUtensorMap* map, void* base, uint64_t all_rows, int rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NB>
+template <int NB, int CODE, int PT>
 lrkv_status launch(const AttnParams& p, int ctas, cudaStream_t s) {
   using C = AttnConfig<NB>;
-  auto kern = p.D.code == LRKV_CODE_INT8
-                  ? (p.D.page == 16 ? attn_kernel<NB, LRKV_CODE_INT8, 16> : attn_kernel<NB, LRKV_CODE_INT8, 32>)
-                  : (p.D.page == 16 ? attn_kernel<NB, LRKV_CODE_E4M3, 16> : attn_kernel<NB, LRKV_CODE_E4M3, 32>);
+  auto kern = p.cap_unit > 0.f || p.slopes ? attn_kernel<NB, CODE, PT, true> : attn_kernel<NB, CODE, PT, false>;
   if (!set_smem(kern, C::kSmem)) return LRKV_ERR_CUDA;
   return launch_pdl(kern, dim3((unsigned)ctas), dim3(C::kThreads), C::kSmem, s, p);
+}
+template <int NB>
+lrkv_status launch(const AttnParams& p, int ctas, cudaStream_t s) {
+  if (p.D.code == LRKV_CODE_INT8)
+    return p.D.page == 16 ? launch<NB, LRKV_CODE_INT8, 16>(p, ctas, s) : launch<NB, LRKV_CODE_INT8, 32>(p, ctas, s);
+  return p.D.page == 16 ? launch<NB, LRKV_CODE_E4M3, 16>(p, ctas, s) : launch<NB, LRKV_CODE_E4M3, 32>(p, ctas, s);
 }
 
 }  // namespace

@@ -415,8 +415,9 @@ __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, floa
                                            : make_uint2(0u, 0u);
 }
 
-// NB: blocks of 8 query rows; CODE: LRKV_CODE_*; PT: tokens of a tile on one page (16 or 32).
-template <int NB, int CODE, int PT>
+// NB: blocks of 8 query rows; CODE: LRKV_CODE_*; PT: tokens of a tile on one page (16 or 32);
+// MOD: scores are capped or get a bias (code that a plain call would have to skip costs it 1 us).
+template <int NB, int CODE, int PT, bool MOD>
 __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using C = AttnConfig<NB>;
   constexpr int W = C::kWarps, kJoin = C::kJoin, ROWS = C::kRows, kRec = C::kRec;   // a record: values [ROWS][kRecRow], references, sums
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           row.lo[j] = a;
           row.hi[j] = z;
           row.pos[j] = (float)i;
-          if (p.slopes) row.slope[j] = p.slopes[h * p.g + r - tok * p.g] * kLog2e;
+          if (MOD && p.slopes) row.slope[j] = p.slopes[h * p.g + r - tok * p.g] * kLog2e;
           all_lo = max(all_lo, a);
           all_hi = min(all_hi, z);
         }
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           f[nb][0][j] = fmaxf(sk0 * row.mul[j], FLT_MIN);   // not 0: an unseen key stays at -inf
           if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = fmaxf(sk1 * row.mul[j], FLT_MIN);
         }
-        if (p.cap_unit > 0.f || p.slopes) {
+        if (MOD) {
 #pragma unroll
           for (int mt = 0; mt < 2; ++mt)
 #pragma unroll

@@ -6,6 +6,8 @@ Every csrc/*.cu (liblrkv.so, include/lrkv.h) and csrc/serve/*.cu
 (liblrkv_serve.so, include/lrkv_serve.h) is compiled to an object on its own
 (in parallel, into _build/), then each library's objects are linked with the
 static CUDA runtime, so the libraries carry no run-time path dependencies.
+_serve_calls.so, the Python binding's fast path, is compiled with g++ against
+torch's headers and Python's.
 """
 import concurrent.futures
 import glob
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblrkv.so")
 SERVE_CSRC = os.path.join(CSRC, "serve")
 SERVE_LIB = os.path.join(PKG, "liblrkv_serve.so")
+CALLS_SRC = os.path.join(SERVE_CSRC, "serve_calls.cpp")
+CALLS_LIB = os.path.join(PKG, "_serve_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -64,8 +69,12 @@ def _newer(lib, inputs):
     return all(os.path.getmtime(f) <= t for f in inputs)
 
 
+def _calls_inputs():
+    return [CALLS_SRC, os.path.join(INCLUDE, "lrkv.h"), os.path.join(INCLUDE, "lrkv_serve.h"), os.path.abspath(__file__)]
+
+
 def up_to_date():
-    return _newer(LIB, _inputs()) and _newer(SERVE_LIB, _serve_inputs())
+    return _newer(LIB, _inputs()) and _newer(SERVE_LIB, _serve_inputs()) and _newer(CALLS_LIB, _calls_inputs())
 
 
 def _compile(src, extra):
@@ -84,6 +93,22 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
+def _build_calls():
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = CALLS_LIB + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", cuda, "-I", INCLUDE, CALLS_SRC, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(tmp, CALLS_LIB)
+
+
 def build(force=False, verbose=False, extra=()):
     """Compile the libraries that are not newer than all their sources; returns liblrkv.so's path."""
     todo = [(lib, srcs) for lib, srcs, inputs in
@@ -91,8 +116,9 @@ def build(force=False, verbose=False, extra=()):
             if force or not _newer(lib, inputs)]
     os.makedirs(OBJ, exist_ok=True)
     srcs = [s for _, part in todo for s in part]
-    workers = max(1, min(len(srcs), os.cpu_count() or 1))
+    workers = max(1, min(len(srcs) + 1, os.cpu_count() or 1))
     with concurrent.futures.ThreadPoolExecutor(workers) as ex:
+        calls = ex.submit(_build_calls) if force or not _newer(CALLS_LIB, _calls_inputs()) else None
         results = dict(zip(srcs, ex.map(lambda s: _compile(s, list(extra)), srcs)))
     for obj, cmd, r in results.values():
         if verbose:
@@ -103,6 +129,8 @@ def build(force=False, verbose=False, extra=()):
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     for lib, part in todo:
         _link([results[s][0] for s in part], lib)
+    if calls is not None:
+        calls.result()
     return LIB
 
 

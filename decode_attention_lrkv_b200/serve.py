@@ -42,6 +42,7 @@ class _PagedCache(ctypes.Structure):
 
 
 _lib = None
+_calls = None    # the calls marshalled in C++ (csrc/serve/serve_calls.cpp)
 
 _SIGNATURES = {
     "lrkv_prefill_workspace_size": (_SZ, [_P]),
@@ -61,7 +62,7 @@ _SIGNATURES = {
 
 def load_serve_library(path=None):
     """Load liblrkv_serve.so (built in-tree).  Raises if it has not been built."""
-    global _lib
+    global _lib, _calls
     if _lib is not None and path is None:
         return _lib
     p = path or SERVE_LIB_PATH
@@ -72,8 +73,22 @@ def load_serve_library(path=None):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     if path is None:
-        _lib = lib
+        try:
+            from . import _serve_calls
+        except ImportError as e:
+            raise RuntimeError("_serve_calls.so is missing: build it with `python -m decode_attention_lrkv_b200.build`") from e
+        _serve_calls.bind([ctypes.cast(getattr(lib, "lrkv_" + n), _P).value for n in (
+            "prefill_workspace_size", "prefill_attn", "paged_append", "paged_read", "paged_attn", "pages_reserve",
+            "pages_advance", "pages_fork", "pages_copy", "pages_free", "pages_compact")])
+        _lib, _calls = lib, _serve_calls
     return lib
+
+
+def _fast():
+    """The calls in C++.  They return -1 for arguments that the Python path has to look at."""
+    if _calls is None:
+        load_serve_library()
+    return _calls
 
 
 class _Fields:
@@ -101,7 +116,9 @@ class Score(_Fields):
 
     def __post_init__(self):
         plain = self.slopes is None and self.first_key is None and self.prefix_end is None
-        object.__setattr__(self, "_plain", ctypes.byref(self.c()) if plain else None)
+        object.__setattr__(self, "_struct", self.c() if plain else None)
+        object.__setattr__(self, "_plain", ctypes.byref(self._struct) if plain else None)
+        object.__setattr__(self, "_at", ctypes.addressof(self._struct) if plain else None)
 
     def c(self):
         return _Score(self.scale, self.softcap, self.window, _addr(self.slopes), _addr(self.first_key),
@@ -121,7 +138,9 @@ class PagedDims(_Fields):
     code: str = "int8"
 
     def __post_init__(self):
-        object.__setattr__(self, "_ref", ctypes.byref(self.c()))
+        object.__setattr__(self, "_struct", self.c())
+        object.__setattr__(self, "_ref", ctypes.byref(self._struct))
+        object.__setattr__(self, "_at", ctypes.addressof(self._struct))
 
     def c(self):
         return _PagedDims(self.B, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages, self.n_layers,
@@ -276,6 +295,9 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
     """out [B,t_q,Hq,d] <- attention of q [B,t_q,Hq,d] over k, v [B,t_k,Hkv,d] (bf16, rows of d contiguous
     elements, otherwise any strides); see include/lrkv_serve.h.  A workspace is made when one is needed
     and none is given."""
+    code = _fast().prefill(q, k, v, out, q_len, kv_len, score, dev_status, ws, stream)
+    if code >= 0:
+        return _done(code, "lrkv_prefill_attn", check)
     device = _device(q, "q")
     _check_rows(q, "q", device)
     _check_rows(k, "k", device)
@@ -316,6 +338,9 @@ def make_paged_workspace(dims, t_q=1, device="cuda"):
 
 def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=None, check=True):
     """Quantise k_new, v_new [B,t_new,Hkv,d] (bf16) into `layer`'s pages at positions seq_len .. ."""
+    code = _fast().append(dims, cache, layer, k_new, v_new, t_new_b, stream)
+    if code >= 0:
+        return _done(code, "lrkv_paged_append", check)
     t_new = k_new.shape[1]
     shape = (dims.B, t_new, dims.Hkv, dims.d)
     device = _device(cache.k, "cache")
@@ -329,6 +354,9 @@ def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=Non
 
 def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None, check=True):
     """Positions first[b] .. first[b] + count[b] - 1 of `layer` as bf16 rows of k_out, v_out [B,t,Hkv,d]."""
+    code = _fast().read(dims, cache, layer, first, count, k_out, v_out, stream)
+    if code >= 0:
+        return _done(code, "lrkv_paged_read", check)
     t_max = k_out.shape[1]
     shape = (dims.B, t_max, dims.Hkv, dims.d)
     device = _device(cache.k, "cache")
@@ -343,6 +371,9 @@ def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None,
 
 def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None, stream=None, check=True):
     """out [B,t_q,Hq,d] <- attention of the newest t_q tokens' queries q (bf16) over `layer`'s pages."""
+    code = _fast().attn(dims, cache, layer, q, out, t_q_b, score, ws, stream)
+    if code >= 0:
+        return _done(code, "lrkv_paged_attn", check)
     t_q = q.shape[1]
     shape = (dims.B, t_q, dims.Hq, dims.d)
     device = _device(cache.k, "cache")
@@ -364,12 +395,18 @@ def _count_call(fn, name, dims, cache, t_new, t_new_b, stream, check):
 
 def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """Pages for t_new (or t_new_b[b]) more tokens of every sequence."""
+    code = _fast().counts(0, dims, cache, t_new, t_new_b, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_reserve", check)
     return _count_call(load_serve_library().lrkv_pages_reserve, "lrkv_pages_reserve", dims, cache, t_new, t_new_b,
                        stream, check)
 
 
 def lrkv_pages_advance(dims, cache, t_new, t_new_b=None, stream=None, check=True):
     """seq_len += t_new (or t_new_b)."""
+    code = _fast().counts(1, dims, cache, t_new, t_new_b, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_advance", check)
     return _count_call(load_serve_library().lrkv_pages_advance, "lrkv_pages_advance", dims, cache, t_new, t_new_b,
                        stream, check)
 
@@ -385,16 +422,25 @@ def _pair_call(fn, name, dims, cache, src, dst, ws, stream, check):
 
 def lrkv_pages_fork(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Sequence dst[i] becomes a copy of sequence src[i] (int32 lists on the device)."""
+    code = _fast().lists(0, dims, cache, src, dst, ws, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_fork", check)
     return _pair_call(load_serve_library().lrkv_pages_fork, "lrkv_pages_fork", dims, cache, src, dst, ws, stream, check)
 
 
 def lrkv_pages_copy(dims, cache, src, dst, ws=None, stream=None, check=True):
     """Copy pages src[i] to dst[i] (int32 lists on the device) in every layer."""
+    code = _fast().lists(1, dims, cache, src, dst, ws, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_copy", check)
     return _pair_call(load_serve_library().lrkv_pages_copy, "lrkv_pages_copy", dims, cache, src, dst, ws, stream, check)
 
 
 def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
     """Empty the sequences listed in seqs (int32, on the device)."""
+    code = _fast().lists(2, dims, cache, seqs, None, None, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_free", check)
     device, n = _device(cache.k, "cache"), seqs.numel()
     _check_list(seqs, "seqs", n, device)
     return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache), seqs.data_ptr(), n,
@@ -403,6 +449,9 @@ def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
 
 def lrkv_pages_compact(dims, cache, ws=None, stream=None, check=True):
     """Move pages so that the live ones have the lowest ids."""
+    code = _fast().lists(3, dims, cache, None, None, ws, stream)
+    if code >= 0:
+        return _done(code, "lrkv_pages_compact", check)
     device = _device(cache.k, "cache")
     n_ws = _check_ws(ws, device)
     return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache), _addr(ws), n_ws,

@@ -325,3 +325,48 @@ def test_binding_refuses_tensors_that_do_not_fit():
         L.lrkv_paged_attn(D, c, 2, bf(2, 1, 4, 128), bf(2, 1, 4, 128), ws=ws)
     with pytest.raises(L.LrkvError):
         L.lrkv_pages_compact(D, c)
+
+
+@pytest.mark.parametrize("scored", [False, True])
+def test_both_paths_of_the_binding_do_the_same(scored):
+    """Ordinary calls are marshalled in C++; an explicit stream takes the Python path."""
+    from decode_attention_lrkv_b200 import serve as S
+    here = torch.cuda.current_stream()
+    results = []
+    for stream in (None, here):
+        D, c, ws = filled(6, 16, 90, 12, n_layers=2)
+        for t in (c.k, c.v):
+            t.zero_()
+        q, k, v = U.normal(1, 6, 40, 4, 128), U.normal(2, 6, 40, 2, 128), U.normal(3, 6, 40, 2, 128)
+        n = U.ints([40, 3, 17, 0, 0, 0])
+        score = L.Score(slopes=U.slopes(4), window=30) if scored else L.Score(softcap=20.0)
+        out, out1 = torch.zeros_like(q), torch.zeros(6, 1, 4, 128, dtype=torch.bfloat16, device="cuda")
+        kk, vv = torch.zeros_like(k), torch.zeros_like(v)
+        kw = dict(stream=stream)
+        L.lrkv_prefill_attn(q, k, v, out, q_len=n, kv_len=n, score=score, **kw)
+        L.lrkv_pages_reserve(D, c, 41, n + 1, **kw)
+        L.lrkv_paged_append(D, c, 1, k, v, t_new_b=n, **kw)
+        L.lrkv_pages_advance(D, c, 40, n, **kw)
+        L.lrkv_paged_read(D, c, 1, None, n, kk, vv, **kw)
+        L.lrkv_pages_fork(D, c, U.ints([0, 1]), U.ints([4, 5]), ws=ws, **kw)
+        L.lrkv_pages_free(D, c, U.ints([1]), **kw)
+        L.lrkv_pages_compact(D, c, ws=ws, **kw)
+        L.lrkv_pages_copy(D, c, U.ints([0]), U.ints([80]), ws=ws, **kw)
+        L.lrkv_paged_append(D, c, 1, k[:, :1].contiguous(), v[:, :1].contiguous(), **kw)
+        L.lrkv_paged_attn(D, c, 1, q[:, :1].contiguous(), out1, score=score, ws=ws, **kw)
+        torch.cuda.synchronize()
+        results.append([out, out1, kk, vv, *(getattr(c, f).clone() for f in c.FIELDS)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    # what each of them takes
+    assert S._calls.counts(1, D, c, 0, None, None) == 0 and S._calls.counts(1, D, c, 0, None, here) == -1
+    twin = L.PagedDims(**{f: getattr(D, f) for f in ("B", "Hq", "Hkv", "d", "page", "n_pages", "max_pages", "n_layers", "code")})
+    assert S._calls.counts(1, twin, c, 0, None, None) == -1      # equal, but another object
+    L.lrkv_pages_advance(twin, c, 0)
+    assert S._calls.append(D, c, 1, k.float(), v, None, None) == -1
+    assert S._calls.append(D, c, 2 ** 40, k, v, None, None) == -1
+    assert S._calls.append(D, c, 7, k, v, None, None) == L.LRKV_ERR_INVALID_ARG
+    assert S._calls.append(D, object(), 1, k, v, None, None) == -1 and S._calls.append(D) == -1
+    assert S._calls.attn(D, c, 1, q, q.cpu(), None, score, ws, None) == -1
+    assert S._calls.attn(D, c, 1, q, out, None, 3, ws, None) == -1
+    assert S._calls.prefill(q, k, v[:, :5], out, None, None, None, None, None, None) == -1
+    assert S._calls.lists(3, D, c, None, None, ws.view(torch.int8), None) == -1

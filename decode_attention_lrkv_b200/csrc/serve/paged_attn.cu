@@ -42,7 +42,14 @@ extern "C" {
 
 size_t lrkv_paged_workspace_size(const lrkv_paged_dims* dims, int32_t t_q) {
   if (paged::check_dims(dims) != LRKV_OK || t_q < 1 || t_q > paged::kMaxTq) return 0;
-  return paged::paged_ws(*dims, t_q).total;
+  // enough for fewer rows too, which may pad to more than t_q does (32 rows fill one block, 36 two
+  // of 24)
+  size_t most = 0;
+  for (int t = 1; t <= t_q; ++t) {
+    const size_t n = paged::paged_ws(*dims, t).total;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache, int32_t layer,

@@ -178,8 +178,8 @@ LRKV_API lrkv_status lrkv_paged_read(const lrkv_paged_dims* dims, const lrkv_pag
  * t_q_b: nullable [B] int32, rows of each sequence (clamped into [0, t_q]); rows
  *   past it are left as they were.
  * t_q: 1 .. 64.
- * ws: lrkv_paged_workspace_size(dims, t_q) bytes, zero-filled once; the calls leave
- *   it as they need it.  One workspace serves one stream of calls (two captured
+ * ws: lrkv_paged_workspace_size(dims, t_q) bytes (for this t_q or a larger one),
+ *   zero-filled once; the calls leave it as they need it.  One workspace serves one stream of calls (two captured
  *   graphs that may run at the same time need one each).
  * Logits and softmax in fp32; queries and weights enter the products as f16
  * (queries scaled by a power of two: exact up to 2^-28 of the row's largest

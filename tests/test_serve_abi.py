@@ -144,6 +144,13 @@ def test_paged_argument_refusals(lib):
     assert lib.lrkv_paged_attn(ctypes.byref(deep), C, 0, A, 1, None, None, A, A, 1 << 40, None) == UNSUP
 
 
+def test_a_workspace_serves_fewer_rows_too(lib):
+    for kw in (dict(Hq=8, Hkv=2), dict(Hq=16, Hkv=2), dict(Hq=6, Hkv=2), dict(max_pages=4), dict(max_pages=1 << 18)):
+        D = _dims(**kw)
+        sizes = [lib.lrkv_paged_workspace_size(ctypes.byref(D), t) for t in range(1, 65)]
+        assert sizes == sorted(sizes), kw
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     D = L.PagedDims(B=2, Hq=4, Hkv=2, d=128, page=16, n_pages=4, max_pages=2)
     cache = L.PagedCache(D, device="cpu")

@@ -10,7 +10,9 @@
 // in place.  Bound by memory: 2 d bytes in and d out per row.
 //
 // Read: eight threads per row, 16 codes in and 32 bytes out each; keys and values of
-// a row by the same threads, two rows in flight.  Bound by memory: d in, 2 d out.
+// a row by the same threads, two rows in flight.  Bound by memory: d in, 2 d out.  32768
+// tokens x 32 heads: append 123 us, read 125 us (6.5 TB/s each); read with two 16-byte stores
+// in place of one of 32 bytes 141 us, with one or four rows in flight 125.
 #include "paged.cuh"
 
 #include "../launch_util.cuh"
@@ -147,6 +149,7 @@ struct ReadParams {
   lrkv_bf16* k_out;
   lrkv_bf16* v_out;
   int layer, t_max;
+  int out32;   // 32-byte stores allowed
 };
 
 constexpr int kReadThreads = 256, kReadRows = 64;   // rows per CTA: two per group of eight threads
@@ -206,8 +209,14 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       }
       uint4* dst = reinterpret_cast<uint4*>((side == 0 ? p.k_out : p.v_out) +
                                             (((size_t)b * p.t_max + i) * D.Hkv + h) * kD + c);
-      __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-      __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      if (p.out32) {   // whole sectors at a time
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]),
+                     "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                     : "memory");
+      } else {
+        __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      }
     }
   }
 }
@@ -275,6 +284,7 @@ lrkv_status lrkv_paged_read(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   p.v_out = v_out;
   p.layer = layer;
   p.t_max = t_max;
+  p.out32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
   const long long gx = (long long)((t_max + paged::kReadRows - 1) / paged::kReadRows) * dims->Hkv;
   if (gx >= (1LL << 31)) return LRKV_ERR_UNSUPPORTED;
   auto kern = dims->code == LRKV_CODE_INT8 ? paged::read_kernel<LRKV_CODE_INT8> : paged::read_kernel<LRKV_CODE_E4M3>;

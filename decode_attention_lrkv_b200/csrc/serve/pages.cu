@@ -500,12 +500,14 @@ lrkv_status list_call(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache
   return LRKV_OK;
 }
 
-// CTAs of a kernel that moves pages: eight to an SM, not more than there is work for.
+// CTAs of a kernel that moves pages: up to 64 for every SM, several waves of those that fit, not
+// more than there may be work for.  Compacting 600 MB: 109 us with 8 for every SM, 99 with 64,
+// 123 with 256.
 unsigned move_grid(const lrkv_paged_dims& D, long long pages, long long rows) {
   const long long pieces = ((long long)page_elems(D) + kMoveBytes - 1) / kMoveBytes;
   long long n = pages * D.n_layers * pieces;
   if (n < rows) n = rows;
-  const long long cap = 8LL * num_sms();
+  const long long cap = 64LL * num_sms();
   return (unsigned)(n < 1 ? 1 : n > cap ? cap : n);
 }
 

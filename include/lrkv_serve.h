@@ -181,6 +181,8 @@ LRKV_API lrkv_status lrkv_paged_read(const lrkv_paged_dims* dims, const lrkv_pag
  * ws: lrkv_paged_workspace_size(dims, t_q) bytes (for this t_q or a larger one),
  *   zero-filled once; the calls leave it as they need it.  One workspace serves one stream of calls (two captured
  *   graphs that may run at the same time need one each).
+ * LRKV_ERR_UNSUPPORTED for a pool of 2^31 rows of codes or more, or a page table with
+ *   room for 2^31 tiles of 32 tokens over all sequences, kv heads and blocks of query rows.
  * Logits and softmax in fp32; queries and weights enter the products as f16
  * (queries scaled by a power of two: exact up to 2^-28 of the row's largest
  * element; weights relative to the row's largest, rounded to 11 bits). */
@@ -192,8 +194,9 @@ LRKV_API lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_pag
 
 /* ---- pages ------------------------------------------------------------------
  * Free pages are those with refs = 0; they are handed out lowest id first, in
- * the order of the sequences (or list entries) that ask.  ws: the workspace of
- * lrkv_paged_attn (any t_q). */
+ * the order of the sequences (or list entries) that ask.  A sequence's row of the
+ * page table is filled from the front.  Lists have at most 2^24 entries.  ws: the
+ * workspace of lrkv_paged_attn (any t_q). */
 
 /* Pages for t_new (or t_new_b[b]) more tokens of every sequence.  A sequence for
  * which the pool, or its row of the page table, does not suffice gets none, nor do
@@ -207,8 +210,9 @@ LRKV_API lrkv_status lrkv_pages_advance(const lrkv_paged_dims* dims, const lrkv_
 
 /* Sequence dst[i] becomes a copy of sequence src[i], for i < n: full pages are
  * shared, a last page that is not full is copied (all layers) to a page of its own.
- * dst[i] has to be empty (seq_len 0 and no pages), and is named once; a source may
- * be named many times.  Sources are taken as they were before the call.
+ * dst[i] has to be empty (seq_len 0 and no pages), and is named once (of entries that
+ * name it again the first counts, LRKV_DEV_BAD_SEQ); a source may be named many times.
+ * Sources are taken as they were before the call.
  * src, dst: device [n] int32. */
 LRKV_API lrkv_status lrkv_pages_fork(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                      const int32_t* src, const int32_t* dst, int32_t n, void* ws,

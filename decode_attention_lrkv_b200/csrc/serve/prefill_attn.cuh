@@ -22,12 +22,14 @@
 // 1024 clocks (1148 measured for the products: S with N = 64 reads shared memory at
 // 48 clocks per step where 32 would do).  A unit of both blocks takes 1700 clocks, and a
 // CTA 11000 more before its first and after its last one.  8192 causal tokens x 32 heads:
-// 474 us (1160 TFLOP/s) at first, 545 us (1009) once the power limit has lowered the clock.
+// 466 us (1180 TFLOP/s) at first, 522 to 545 us once the power limit has lowered the clock.
 // Also measured, each at first / under the power limit: the softmax groups taking their
 // exponentials in turn, one thread issuing all of a block's MMAs, 473 / 578 us; tiles of
 // 128 keys, whose S waits for O += P V of the tile before, 511 / 572; those with P in two
 // halves, 526 / 586; a quarter or half of the exponentials by a cubic polynomial, which is
-// 10 clocks of work on the fp32 pipe against 8 on the special-function unit, no faster.
+// 10 clocks of work on the fp32 pipe against 8 on the special-function unit, no faster.  One
+// row block per CTA and two CTAs to an SM, which loads keys and values twice, takes the same
+// time here (465 against 466 us, 519 against 522) and more with documents (268 against 257).
 //
 // The running reference m only moves when a row's maximum passes it by more than
 // 2^24 (bf16 and fp32 weights up to 2^24 are as exact as others): O is rescaled in tensor

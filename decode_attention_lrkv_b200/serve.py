@@ -153,7 +153,8 @@ class PagedCache:
     k, v: uint8 [n_layers, n_pages, Hkv, page, d]; scale_k, scale_v: fp32 [n_layers,
     n_pages, Hkv]; int32 page_table [B, max_pages] (-1: no page), seq_len [B], refs
     [n_pages]; dev_status int32 [4] (word 0 used).  Tensors that the caller already
-    has may be given by name; the others are made for a new, empty cache.
+    has may be given by name; the others are made for a new, empty cache.  All lie on one
+    device.  A tensor may be replaced by one of the same shape, type and device; dims stay.
     """
     FIELDS = ("k", "v", "scale_k", "scale_v", "page_table", "seq_len", "refs", "dev_status")
 
@@ -164,18 +165,30 @@ class PagedCache:
                   "page_table": ((D.B, D.max_pages), torch.int32), "seq_len": ((D.B,), torch.int32),
                   "refs": ((D.n_pages,), torch.int32), "dev_status": ((4,), torch.int32)}
         shapes["v"], shapes["scale_v"] = shapes["k"], shapes["scale_k"]
+        unknown = [name for name in given if name not in shapes]
+        if unknown:
+            raise TypeError(f"PagedCache has no {', '.join(unknown)}")
+        given = {name: t for name, t in given.items() if t is not None}
         if given:
             device = next(iter(given.values())).device
+        self._shapes, self.dims = shapes, dims
         for name in self.FIELDS:
             shape, dtype = shapes[name]
-            t = given.pop(name, None)
+            t = given.get(name)
             if t is None:
                 t = torch.full(shape, -1 if name == "page_table" else 0, dtype=dtype, device=device)
-            _check(t, name, shape, dtype)
             setattr(self, name, t)
-        if given:
-            raise TypeError(f"PagedCache has no {', '.join(given)}")
-        self.dims = dims
+
+    def __setattr__(self, name, value):
+        # the calls take the tensors' addresses, and the sizes from dims
+        if name in self.FIELDS:
+            _check(value, name, *self._shapes[name])
+            other = next((t for f in self.FIELDS if f != name and (t := self.__dict__.get(f)) is not None), value)
+            if value.device != other.device:
+                raise ValueError(f"{name}: the cache's other tensors are on {other.device}, this one is on {value.device}")
+        elif name in self.__dict__:
+            raise AttributeError(f"a PagedCache's {name} cannot be replaced")
+        object.__setattr__(self, name, value)
 
     def c(self):
         return _PagedCache(self.k.data_ptr(), self.v.data_ptr(), self.scale_k.data_ptr(), self.scale_v.data_ptr(),
@@ -253,9 +266,13 @@ def _ref(score):
     return score._plain if score._plain is not None else ctypes.byref(score.c())
 
 
-def _cache_ref(dims, cache):
+def _cache_ref(dims, cache, device):
     if cache.dims is not dims and cache.dims != dims:
         raise ValueError(f"the cache was made for {cache.dims}, not {dims}")
+    for name in cache.FIELDS:
+        t = getattr(cache, name)
+        if t.get_device() != device:
+            _wrong_device(t, name, device)
     return ctypes.byref(cache.c())
 
 
@@ -348,7 +365,7 @@ def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=Non
     _check(v_new, "v_new", shape, torch.bfloat16, device)
     _check_list(t_new_b, "t_new_b", dims.B, device)
     return _done(load_serve_library().lrkv_paged_append(
-        dims._ref, _cache_ref(dims, cache), layer, k_new.data_ptr(), v_new.data_ptr(), t_new, _addr(t_new_b),
+        dims._ref, _cache_ref(dims, cache, device), layer, k_new.data_ptr(), v_new.data_ptr(), t_new, _addr(t_new_b),
         _stream(stream, device)), "lrkv_paged_append", check)
 
 
@@ -365,7 +382,7 @@ def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None,
     _check_list(first, "first", dims.B, device)
     _check_list(count, "count", dims.B, device)
     return _done(load_serve_library().lrkv_paged_read(
-        dims._ref, _cache_ref(dims, cache), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
+        dims._ref, _cache_ref(dims, cache, device), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
         v_out.data_ptr(), _stream(stream, device)), "lrkv_paged_read", check)
 
 
@@ -383,14 +400,14 @@ def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None,
     _check_score(score, dims.B, t_q, dims.Hq, device)
     n_ws = _check_ws(ws, device)
     return _done(load_serve_library().lrkv_paged_attn(
-        dims._ref, _cache_ref(dims, cache), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score), out.data_ptr(),
+        dims._ref, _cache_ref(dims, cache, device), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score), out.data_ptr(),
         _addr(ws), n_ws, _stream(stream, device)), "lrkv_paged_attn", check)
 
 
 def _count_call(fn, name, dims, cache, t_new, t_new_b, stream, check):
     device = _device(cache.k, "cache")
     _check_list(t_new_b, "t_new_b", dims.B, device)
-    return _done(fn(dims._ref, _cache_ref(dims, cache), t_new, _addr(t_new_b), _stream(stream, device)), name, check)
+    return _done(fn(dims._ref, _cache_ref(dims, cache, device), t_new, _addr(t_new_b), _stream(stream, device)), name, check)
 
 
 def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True):
@@ -416,7 +433,7 @@ def _pair_call(fn, name, dims, cache, src, dst, ws, stream, check):
     _check_list(src, "src", n, device)
     _check_list(dst, "dst", n, device)
     n_ws = _check_ws(ws, device)
-    return _done(fn(dims._ref, _cache_ref(dims, cache), src.data_ptr(), dst.data_ptr(), n, _addr(ws), n_ws,
+    return _done(fn(dims._ref, _cache_ref(dims, cache, device), src.data_ptr(), dst.data_ptr(), n, _addr(ws), n_ws,
                     _stream(stream, device)), name, check)
 
 
@@ -443,7 +460,7 @@ def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
         return _done(code, "lrkv_pages_free", check)
     device, n = _device(cache.k, "cache"), seqs.numel()
     _check_list(seqs, "seqs", n, device)
-    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache), seqs.data_ptr(), n,
+    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache, device), seqs.data_ptr(), n,
                                                       _stream(stream, device)), "lrkv_pages_free", check)
 
 
@@ -454,5 +471,5 @@ def lrkv_pages_compact(dims, cache, ws=None, stream=None, check=True):
         return _done(code, "lrkv_pages_compact", check)
     device = _device(cache.k, "cache")
     n_ws = _check_ws(ws, device)
-    return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache), _addr(ws), n_ws,
+    return _done(load_serve_library().lrkv_pages_compact(dims._ref, _cache_ref(dims, cache, device), _addr(ws), n_ws,
                                                          _stream(stream, device)), "lrkv_pages_compact", check)

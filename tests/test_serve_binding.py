@@ -1,0 +1,52 @@
+"""What the Python binding of the serving calls refuses by itself, without a GPU."""
+import copy
+import pickle
+
+import pytest
+import torch
+
+import decode_attention_lrkv_b200 as L
+from decode_attention_lrkv_b200 import serve as S
+
+
+def small(**kw):
+    return L.PagedDims(**{**dict(B=2, Hq=4, Hkv=2, d=128, page=16, n_pages=4, max_pages=2), **kw})
+
+
+def test_a_cache_lies_on_one_device():
+    D = small()
+    codes = torch.empty(1, 4, 2, 16, 128, dtype=torch.uint8, device="meta")
+    table = torch.full((2, 2), -1, dtype=torch.int32)
+    for given in (dict(k=codes, page_table=table), dict(page_table=table, v=codes)):
+        with pytest.raises(ValueError, match="other tensors are on"):
+            L.PagedCache(D, **given)
+    c = L.PagedCache(D, device="cpu")
+    with pytest.raises(ValueError, match="other tensors are on"):
+        c.k = codes
+    # and the calls look at each of them
+    for name in c.FIELDS:
+        mixed = L.PagedCache(D, device="cpu")
+        fake = {n: torch.empty_like(getattr(mixed, n), device="meta") for n in c.FIELDS if n != name}
+        for t in fake.values():
+            t.get_device = lambda: 0
+        mixed.__dict__.update(fake)
+        with pytest.raises(ValueError, match=f"^{name}: a CUDA tensor on cuda:0 is needed"):
+            S._cache_ref(D, mixed, 0)
+
+
+def test_a_cache_keeps_its_shapes():
+    D = small()
+    c = L.PagedCache(D, device="cpu")
+    for name, bad in (("page_table", torch.zeros(2, 1, dtype=torch.int32)), ("seq_len", torch.zeros(2, dtype=torch.int64)),
+                      ("k", c.k[:, :3]), ("scale_v", c.scale_v.transpose(1, 2)), ("refs", torch.zeros(3, dtype=torch.int32))):
+        with pytest.raises(ValueError, match=name):
+            setattr(c, name, bad)
+    with pytest.raises(AttributeError, match="dims"):
+        c.dims = small(max_pages=9)
+    table = torch.full((2, 2), -1, dtype=torch.int32)
+    c.page_table = table
+    assert c.page_table is table and c.c().page_table == table.data_ptr()
+    with pytest.raises(TypeError, match="no keys"):
+        L.PagedCache(D, device="cpu", keys=table)
+    for other in (copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert other.dims == D and all(torch.equal(getattr(other, n), getattr(c, n)) for n in c.FIELDS)

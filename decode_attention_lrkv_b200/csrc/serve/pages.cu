@@ -29,6 +29,8 @@ struct PageParams {
   int half;                 // max(n_pages, B)
 };
 
+__device__ __forceinline__ bool in_range(int v, int n) { return v >= 0 && v < n; }
+
 // Exclusive prefix sum over the block; *total: the sum (in every thread).
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -155,17 +157,31 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const __grid_cons
   if (status) atomicOr(p.C.dev_status, status);
 }
 
-__global__ void advance_kernel(const __grid_constant__ PageParams p) {
+// A warp per sequence: its lanes look through the table entries that the new tokens need, all of
+// them (no early end, so the loads do not wait for one another).
+__global__ void __launch_bounds__(kMoveThreads) advance_kernel(const __grid_constant__ PageParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  const int b = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= p.D.B) return;
   uint32_t status = 0;
   const int n = call_tokens(p.t_new_b, b, p.t_new, &status);
   const int cap = p.D.max_pages * p.D.page;
   const int len = min(max(p.C.seq_len[b], 0), cap);
   if (len + n > cap) status |= LRKV_DEV_SEQ_OVERFLOW;
-  p.C.seq_len[b] = min(len + n, cap);
+  int stop = min(len + n, cap);
+  // the first slot that has no page: the tokens from there on were never stored
+  const int* row = p.C.page_table + (size_t)b * p.D.max_pages;
+  const int end = (stop + p.D.page - 1) / p.D.page;
+  int hole = end;
+  if (stop > len)
+#pragma unroll 4
+    for (int s = len / p.D.page + lane; s < end; s += 32)
+      if (!in_range(row[s], p.D.n_pages)) hole = min(hole, s);
+  hole = __reduce_min_sync(0xffffffffu, hole);
+  if (hole < end) status |= LRKV_DEV_BAD_PAGE, stop = max(len, hole * p.D.page);
+  if (lane != 0) return;
+  p.C.seq_len[b] = stop;
   if (status) atomicOr(p.C.dev_status, status);
 }
 
@@ -221,7 +237,6 @@ __device__ __forceinline__ void move_listed(const PageParams& p) {
 // none), len[b] its length, own[b] = 1 + the place of b's own last page in the list of
 // pages to move (0: it has none).
 
-__device__ __forceinline__ bool in_range(int v, int n) { return v >= 0 && v < n; }
 __device__ __forceinline__ int* list_part(const PageParams& p, int k) { return p.list + 4 + (size_t)k * p.half; }
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_constant__ PageParams p) {
@@ -542,7 +557,8 @@ lrkv_status lrkv_pages_advance(const lrkv_paged_dims* dims, const lrkv_paged_cac
   PageParams p = {};
   const lrkv_status st = count_call(dims, cache, t_new, t_new_b, &p);
   if (st != LRKV_OK || t_new == 0) return st;
-  return launch_pdl(advance_kernel, dim3((unsigned)((dims->B + 255) / 256)), dim3(256), 0,
+  constexpr int kWarps = kMoveThreads / 32;
+  return launch_pdl(advance_kernel, dim3((unsigned)((dims->B + kWarps - 1) / kWarps)), dim3(kMoveThreads), 0,
                     static_cast<cudaStream_t>(stream), p);
 }
 

@@ -33,7 +33,8 @@ extern "C" {
 
 /* Further bits of a status word (see LRKV_DEV_* in lrkv.h). */
 #define LRKV_DEV_BAD_PAGE 0x10u  /* a page id outside [0, n_pages) where one was needed:
-                                    its tokens were skipped (not written, not attended) */
+                                    its tokens were skipped (not written, not attended, not
+                                    counted by lrkv_pages_advance) */
 #define LRKV_DEV_NO_PAGES 0x20u  /* the pool ran out: the sequence (or fork) that did not
                                     fit, and those after it in the call, got nothing */
 #define LRKV_DEV_BAD_SEQ 0x40u   /* a sequence index out of range or listed twice, a fork
@@ -204,7 +205,9 @@ LRKV_API lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_pag
 LRKV_API lrkv_status lrkv_pages_reserve(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                         int32_t t_new, const int32_t* t_new_b, void* stream);
 
-/* seq_len[b] += t_new (or t_new_b[b]), at most max_pages * page. */
+/* seq_len[b] += t_new (or t_new_b[b]), at most max_pages * page (LRKV_DEV_SEQ_OVERFLOW) and
+ * never over a token whose table entry is no page: a sequence to which lrkv_pages_reserve gave
+ * nothing stops in front of its first such token (LRKV_DEV_BAD_PAGE). */
 LRKV_API lrkv_status lrkv_pages_advance(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                         int32_t t_new, const int32_t* t_new_b, void* stream);
 

@@ -117,9 +117,21 @@ class Pool:
                 self.table[b][slot + i] = free[i]
                 self.refs[free[i]] = 1
 
+    def page_ok(self, b, slot):
+        return 0 <= self.table[b][slot] < len(self.refs)
+
     def advance(self, counts):
         for b, n in enumerate(counts):
-            self.len[b] = min(self.len[b] + n, len(self.table[b]) * self.page)
+            if self.len[b] + n > len(self.table[b]) * self.page:
+                self.status |= 0x2
+            for _ in range(n):                   # token by token, to the first that has no page
+                slot = self.len[b] // self.page
+                if slot >= len(self.table[b]):
+                    break
+                if not self.page_ok(b, slot):
+                    self.status |= 0x10
+                    break
+                self.len[b] += 1
 
     def fork(self, src, dst):
         B = len(self.table)

@@ -1,10 +1,14 @@
 """Calls of the serving operators that the other tests do not make: wrong devices, sequences whose
 pages ran out, rejected drafts, weights far below the largest one, numbers that are not finite."""
+import random
+
 import pytest
 import torch
 
 import decode_attention_lrkv_b200 as L
 from tests import serve_testutil as U
+from tests.test_gpu_paged import attn, check
+from tests.test_gpu_pages import contents, filled, host, random_state, same
 
 pytestmark = pytest.mark.gpu
 CANARY = 123.0
@@ -29,3 +33,65 @@ def test_a_cache_with_a_tensor_of_the_host_is_refused(name):
                      lambda: L.lrkv_pages_copy(D, c, one, one, ws=ws, **kw), lambda: L.lrkv_pages_compact(D, c, ws=ws, **kw)):
             with pytest.raises(ValueError, match="CUDA tensor"):
                 call()
+
+
+# ---- sequences that got no pages -----------------------------------------------------
+
+
+@pytest.mark.parametrize("B,page,max_pages", [(1, 16, 3), (9, 16, 40), (40, 128, 5), (300, 32, 70)])
+def test_advance_stops_where_pages_are_missing(B, page, max_pages):
+    D, c, ws = filled(B, page, B * max_pages + 5, max_pages, n_layers=1, Hkv=1)
+    for seed in range(6):
+        rng = random.Random(seed)
+        random_state(c, seed)
+        table = c.page_table.tolist()
+        for b in range(B):
+            have = rng.randint(0, max_pages)
+            table[b][:have] = [rng.randrange(D.n_pages) for _ in range(have)]
+            if rng.random() < 0.3:
+                table[b][rng.randrange(max_pages)] = rng.choice([-1, D.n_pages, 10 ** 9, -5])
+        c.page_table.copy_(U.ints(table))
+        c.dev_status.zero_()
+        pool, before = host(c), contents(c)
+        counts = [rng.choice([0, 1, 2, page, rng.randint(0, page * max_pages)]) for _ in range(B)]
+        one = seed == 5
+        L.lrkv_pages_advance(D, c, max(counts), None if one else U.ints(counts))
+        pool.advance([max(counts)] * B if one else counts)
+        same(c, pool, before)
+
+
+def test_a_pool_that_runs_out_in_the_middle_of_a_run():
+    """The steps of a serving loop on a pool that is full: once another sequence has gone, the one
+    that had to wait goes on where it stopped, and sees nothing of what its new page held before."""
+    D = L.PagedDims(B=2, Hq=4, Hkv=2, d=128, page=16, n_pages=3, max_pages=4)
+    c, ws = L.PagedCache(D), L.make_paged_workspace(D)
+    k, v = U.normal(1, 2, 32, 2, 128), U.normal(2, 2, 32, 2, 128) * 50
+    n = U.ints([16, 32])
+    L.lrkv_pages_reserve(D, c, 32, n)
+    L.lrkv_paged_append(D, c, 0, k, v, t_new_b=n)
+    L.lrkv_pages_advance(D, c, 32, n)
+    assert c.seq_len.tolist() == [16, 32] and int(c.dev_status[0]) == 0
+    one = U.ints([1, 0])
+
+    def step(seed):
+        L.lrkv_pages_reserve(D, c, 1, one)
+        k1, v1 = U.normal(seed, 2, 1, 2, 128), U.normal(seed + 1, 2, 1, 2, 128)
+        L.lrkv_paged_append(D, c, 0, k1, v1, t_new_b=one)
+        q = U.normal(seed + 2, 2, 1, 4, 128)
+        out = attn(D, c, q, [1, 0], ws=ws)
+        L.lrkv_pages_advance(D, c, 1, one)
+        return q, out, k1, v1
+
+    for i in range(2):
+        step(10 + i)
+        assert c.seq_len.tolist() == [16, 32] and c.page_table[0].tolist() == [0, -1, -1, -1]
+    assert int(c.dev_status[0]) == L.DEV_NO_PAGES | L.DEV_BAD_PAGE
+    c.dev_status.zero_()
+    L.lrkv_pages_free(D, c, U.ints([1]))
+    q, out, k1, v1 = step(20)
+    assert c.seq_len.tolist() == [17, 0] and int(c.dev_status[0]) == 0
+    c.seq_len[0] = 16
+    check(out, D, c, q, [1, 0])
+    # the new page's scale is that of its one token alone
+    page = int(c.page_table[0, 1])
+    assert torch.equal(c.scale_v[0, page].cpu(), (v1[0, 0].float().abs().amax(1).cpu() / torch.full((2,), 127.0)))

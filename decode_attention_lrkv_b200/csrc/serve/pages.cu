@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const __grid_co
         if (T % p.D.page) {
           page = p.C.page_table[(size_t)s * p.D.max_pages + T / p.D.page];
           part = in_range(page, p.D.n_pages);
-          if (!part) status |= LRKV_DEV_BAD_PAGE;
+          if (!part) status |= LRKV_DEV_BAD_PAGE, d = -1;   // the source's own last tokens are not there
         }
       } else {
         status |= LRKV_DEV_BAD_SEQ;

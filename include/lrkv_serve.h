@@ -215,7 +215,8 @@ LRKV_API lrkv_status lrkv_pages_advance(const lrkv_paged_dims* dims, const lrkv_
  * shared, a last page that is not full is copied (all layers) to a page of its own.
  * dst[i] has to be empty (seq_len 0 and no pages), and is named once (of entries that
  * name it again the first counts, LRKV_DEV_BAD_SEQ); a source may be named many times.
- * Sources are taken as they were before the call.
+ * Sources are taken as they were before the call; an entry whose source has no page for its
+ * last tokens is skipped (LRKV_DEV_BAD_PAGE).
  * src, dst: device [n] int32. */
 LRKV_API lrkv_status lrkv_pages_fork(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                      const int32_t* src, const int32_t* dst, int32_t n, void* ws,

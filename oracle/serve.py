@@ -144,6 +144,9 @@ class Pool:
             if not (0 <= s < B and fresh and s != d and was[d] == 0 and self.table[d][0] < 0):
                 self.status |= 0x40
                 continue
+            if was[s] % self.page and not self.page_ok(s, was[s] // self.page):
+                self.status |= 0x10
+                continue
             plan.append((s, d))
         old = [list(r) for r in self.table]
         free = self.free_ids()

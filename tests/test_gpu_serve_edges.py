@@ -8,7 +8,7 @@ import torch
 import decode_attention_lrkv_b200 as L
 from tests import serve_testutil as U
 from tests.test_gpu_paged import attn, check
-from tests.test_gpu_pages import contents, filled, host, random_state, same
+from tests.test_gpu_pages import contents, filled, host, random_state, same, set_state
 
 pytestmark = pytest.mark.gpu
 CANARY = 123.0
@@ -95,3 +95,14 @@ def test_a_pool_that_runs_out_in_the_middle_of_a_run():
     # the new page's scale is that of its one token alone
     page = int(c.page_table[0, 1])
     assert torch.equal(c.scale_v[0, page].cpu(), (v1[0, 0].float().abs().amax(1).cpu() / torch.full((2,), 127.0)))
+
+
+def test_fork_of_a_source_without_its_last_page():
+    for bad in (-1, 60, 10 ** 9):
+        D, c, ws = filled(5, 16, 60, 4)
+        set_state(c, [[3, bad, -1, -1], [4, 5, -1, -1]] + [[-1] * 4] * 3, [0] * 3 + [1] * 3 + [0] * 54, [20, 30, 0, 0, 0])
+        pool, before = host(c), contents(c)
+        L.lrkv_pages_fork(D, c, U.ints([0, 1, 0]), U.ints([2, 3, 4]), ws=ws)
+        pool.fork([0, 1, 0], [2, 3, 4])
+        assert pool.len == [20, 30, 0, 30, 0] and pool.status == L.DEV_BAD_PAGE
+        same(c, pool, before)

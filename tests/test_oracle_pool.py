@@ -13,3 +13,10 @@ def test_a_sequence_does_not_advance_over_tokens_without_a_page():
     p = R.Pool([[0, 1]], [1, 1], [7], 4)
     p.advance([2])
     assert p.len == [8] and p.status == 0x2
+
+
+def test_a_source_without_its_last_page_is_not_forked():
+    p = R.Pool([[0, -1], [1, 2], [-1, -1], [-1, -1]], [1, 1, 1, 0, 0], [6, 8, 0, 0], 4)
+    p.fork([0, 1], [2, 3])
+    assert p.table == [[0, -1], [1, 2], [-1, -1], [1, 2]] and p.len == [6, 8, 0, 8]
+    assert p.refs == [1, 2, 2, 0, 0] and p.moves == [] and p.status == 0x10

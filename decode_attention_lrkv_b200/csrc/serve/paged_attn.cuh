@@ -218,18 +218,21 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Codes to f16x2 of the word's bytes (0, 1) and (2, 3), exactly; int8 codes with 1152
-// added: a byte with its sign bit flipped is code + 128, and the f16 with high byte 0x64
-// and that low byte is 1024 more.  The sums that such operands enter start from what the
+// Codes to f16x2 of the word's bytes (0, 1) and (2, 3), exactly; int8 codes as (code + 128) 2^-24:
+// a byte with its sign bit flipped is code + 128, and a subnormal f16 with that low byte has
+// that value in units of 2^-24.  The sums that such operands enter start from what the
 // shift adds to them, with the sign turned.  (Taking the shift off every operand instead,
 // by two more instructions per word: 168 against 164 us at 131072 tokens x 32 heads, 182 against
-// 174 under the power limit; 89 against 81 us for sixteen sequences of 8K to 16K x 8 heads.)
+// 174 under the power limit; 89 against 81 us for sixteen sequences of 8K to 16K x 8 heads.  As
+// normal numbers, with high byte 0x64, codes would come with 1152 added, at the cost of three
+// bits of the sums.)
+constexpr float kCodeUnit = 1.f / 16777216.f;   // of int8 codes as operands
 template <int CODE>
 __device__ __forceinline__ void codes_pairs(uint32_t w, uint32_t& h01, uint32_t& h23) {
   if (CODE == LRKV_CODE_INT8) {
     const uint32_t u = w ^ 0x80808080u;
-    h01 = __byte_perm(u, 0x64646464u, 0x4140);
-    h23 = __byte_perm(u, 0x64646464u, 0x4342);
+    h01 = __byte_perm(u, 0u, 0x4140);
+    h23 = __byte_perm(u, 0u, 0x4342);
   } else {
     codes_f16<CODE>(w, h01, h23);
   }
@@ -239,8 +242,8 @@ template <int CODE>
 __device__ __forceinline__ void codes_evenodd(uint32_t w, uint32_t& h02, uint32_t& h13) {
   if (CODE == LRKV_CODE_INT8) {
     const uint32_t u = w ^ 0x80808080u;
-    h02 = __byte_perm(u, 0x64646464u, 0x4240);
-    h13 = __byte_perm(u, 0x64646464u, 0x4341);
+    h02 = __byte_perm(u, 0u, 0x4240);
+    h13 = __byte_perm(u, 0u, 0x4341);
   } else {
     const uint32_t r = __byte_perm(w, 0, 0x3120);
     h02 = e4m3x2_f16x2(r & 0xffffu);
@@ -525,6 +528,12 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     }
     return ok;
   };
+  // From a raw product to a score in log2 units; positive and finite: an unseen key stays at -inf,
+  // a product of 0 at 0.
+  auto factor = [](float scale, float mul) {
+    const float f = scale * mul;
+    return fminf(fmaxf(kInt ? f * (1.f / kCodeUnit) : f, FLT_MIN), FLT_MAX);
+  };
   // The unit has been read: bring the next one into its slot.
   auto next_unit = [&]() {
     slot = slot + 1 == C::kUnits ? 0 : slot + 1;
@@ -555,7 +564,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
     uint32_t qf[C::kQShared ? 1 : NB][8][2];
     float m[NB][2], l[NB][2];
     int all_lo = 0, all_hi = 0x7fffffff;   // keys that every row sees
-    const uint32_t minus_shift[4] = {0xE480E480u, 0xE480E480u, 0xE480E480u, 0xE480E480u};   // f16x2 (-1152, -1152)
+    const uint32_t minus_shift[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};   // f16x2 of -128 units
     __syncwarp();
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) m[nb][0] = m[nb][1] = -INFINITY, l[nb][0] = l[nb][1] = 0.f;
@@ -679,8 +688,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
         const typename C::Row2& row = sh.row[warp][nb][t4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          f[nb][0][j] = fmaxf(sk0 * row.mul[j], FLT_MIN);   // not 0: an unseen key stays at -inf
-          if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = fmaxf(sk1 * row.mul[j], FLT_MIN);
+          f[nb][0][j] = factor(sk0, row.mul[j]);
+          if (PT == 16) f[nb][PT == 16 ? 1 : 0][j] = factor(sk1, row.mul[j]);
         }
         if (MOD) {
 #pragma unroll
@@ -816,6 +825,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 4);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
+        if (kInt) l[nb][j] *= kCodeUnit;   // the unit of the values' sums
       }
     if (at.tile == 0 && n_tiles == at.s.tiles) {   // the whole segment: write it
 #pragma unroll

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import decode_attention_lrkv_b200 as L
+from oracle import serve as R
 from tests import serve_testutil as U
 from tests.test_gpu_paged import attn, check
 from tests.test_gpu_pages import contents, filled, host, random_state, same, set_state
@@ -106,3 +107,41 @@ def test_fork_of_a_source_without_its_last_page():
         pool.fork([0, 1, 0], [2, 3, 4])
         assert pool.len == [20, 30, 0, 30, 0] and pool.status == L.DEV_BAD_PAGE
         same(c, pool, before)
+
+
+# ---- numbers -------------------------------------------------------------------------
+
+
+def small_codes(T, page, kstd, vtop, q, seed):
+    """One kv head of int8 keys of deviation 1 (kstd codes) and values of -vtop .. vtop codes."""
+    n = T // page + 1
+    D = L.PagedDims(B=1, Hq=q.shape[2], Hkv=1, d=128, page=page, n_pages=n, max_pages=n, code="int8")
+    c = L.PagedCache(D)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = (torch.randn(n * page, 128, generator=g, device="cuda") * kstd).clamp(-127, 127).round()
+    v = torch.randint(-vtop, vtop + 1, (n * page, 128), generator=g, device="cuda")
+    for name, x in (("k", k), ("v", v)):
+        getattr(c, name).copy_(x.to(torch.int8).view(torch.uint8).view(n, page, 128)[None, :, None])
+    c.scale_k.fill_(1 / kstd), c.scale_v.fill_(1.0)
+    c.page_table.copy_(torch.arange(n, device="cuda")), c.seq_len.fill_(T - 1)
+    return D, c, k[:T].double() * float(c.scale_k[0, 0, 0]), v[:T].double()
+
+
+@pytest.mark.parametrize("T,page", [(64, 64), (8192, 16), (65536, 64), (200000, 128)])
+@pytest.mark.parametrize("kstd,sign", [(36.0, False), (2.0, True)])
+def test_small_codes_over_many_tokens(T, page, kstd, sign):
+    """Values of a few code steps on pages whose scale a louder token has set, and queries of one
+    sign: what the shift of int8 codes adds has to leave the sums without a trace.  The output is a
+    sum of values of random signs, so independent errors of the weights are off it by 2^-11 / sqrt 3
+    relative to it, the last rounding by 2^-8 / sqrt 3 at most (root mean square); fp32 sums of
+    codes below 2^8 have ten bits to spare.  2^-8 holds for all together."""
+    q = U.normal(5, 1, 1, 8, 128)
+    q = q.abs() if sign else q
+    D, c, k, v = small_codes(T, page, kstd, 1, q, 1)
+    out = attn(D, c, q)
+    pos = torch.tensor([T - 1], device="cuda")
+    err = size = 0.0
+    for h in range(8):
+        ref = R.attend(q[0, :, h], k, v, pos, pos * 0, pos)[0]
+        err, size = err + float(((out[0, :, h].double() - ref) ** 2).sum()), size + float((ref ** 2).sum())
+    assert err <= size * U.U ** 2, (err / size) ** 0.5

@@ -36,6 +36,10 @@ namespace paged {
 constexpr int kTile = 32;                // tokens
 constexpr int kUnitBytes = kTile * kD;   // codes of a tile's keys, or of its values
 constexpr float kLazyMax = 8.f;          // rescale when a maximum grows by more (log2)
+// Weights are formed 2^7 times as large, up to 2^15, the top of f16's range: its smallest step is
+// then 2^-31 of the reference's weight.  (Without it, weights below 2^-25 became zero in the
+// products and still counted in the sum that divides them.)
+constexpr float kLift = 7.f, kUnlift = 1.f / 128.f;
 
 struct AttnParams {
   CUtensorMap map_k, map_v;   // codes as rows of 128 bytes; box {128, min(page, 32)}
@@ -757,7 +761,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
       uint32_t pf[NB][2][2];   // weights as B fragments
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float ref0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], ref1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
+        const float ref0 = (m[nb][0] == -INFINITY ? 0.f : m[nb][0]) - kLift;
+        const float ref1 = (m[nb][1] == -INFINITY ? 0.f : m[nb][1]) - kLift;
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -782,7 +787,9 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
 
       if (!wait_unit()) break;
       unsigned char* vt = ring + slot * kUnitBytes;
-      const float sv0 = sh.scale[warp][slot][0], sv1 = PT == 16 ? sh.scale[warp][slot][1] : sv0;
+      // results: e4m3 in plain units; int8 in 2^-17, which the sums of weights are brought to as well
+      constexpr float kValue = kInt ? 1.f : kUnlift;
+      const float sv0 = sh.scale[warp][slot][0] * kValue, sv1 = PT == 16 ? sh.scale[warp][slot][1] * kValue : sv0;
       if (!kInt && gone) {   // what lies there may be a NaN, which a zero weight keeps: clear those rows
         if (gone >> lane & 1) {
 #pragma unroll
@@ -825,7 +832,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 4);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 8);
         l[nb][j] += __shfl_xor_sync(0xffffffffu, l[nb][j], 16);
-        if (kInt) l[nb][j] *= kCodeUnit;   // the unit of the values' sums
+        l[nb][j] *= kInt ? kCodeUnit : kUnlift;
       }
     if (at.tile == 0 && n_tiles == at.s.tiles) {   // the whole segment: write it
 #pragma unroll

@@ -186,7 +186,9 @@ LRKV_API lrkv_status lrkv_paged_read(const lrkv_paged_dims* dims, const lrkv_pag
  *   room for 2^31 tiles of 32 tokens over all sequences, kv heads and blocks of query rows.
  * Logits and softmax in fp32; queries and weights enter the products as f16
  * (queries scaled by a power of two: exact up to 2^-28 of the row's largest
- * element; weights relative to the row's largest, rounded to 11 bits). */
+ * element; weights rounded to 11 bits down to 2^-21 of the row's largest, to steps of at
+ * most 2^-31 of it below that; the sum that divides them is not rounded).  int8 codes
+ * enter the fp32 sums with 128 added, which is taken off again. */
 LRKV_API size_t lrkv_paged_workspace_size(const lrkv_paged_dims* dims, int32_t t_q);
 LRKV_API lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                      int32_t layer, const lrkv_bf16* q, int32_t t_q,

@@ -145,3 +145,29 @@ def test_small_codes_over_many_tokens(T, page, kstd, sign):
         ref = R.attend(q[0, :, h], k, v, pos, pos * 0, pos)[0]
         err, size = err + float(((out[0, :, h].double() - ref) ** 2).sum()), size + float((ref ** 2).sum())
     assert err <= size * U.U ** 2, (err / size) ** 0.5
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("Hq,t_q", [(4, 1), (4, 8)])
+def test_many_weights_far_below_the_largest_one(Hq, t_q, page):
+    """The first key of every 32 has a value of zero and lies 15 to 20 nats above the others, whose
+    weights are all that the output is made of.  A weight of 2^-21 of the largest one or more is off
+    by 2^-11 of itself, a smaller one by 2^-32 of the largest (half of f16's smallest step, lifted 2^7)."""
+    T = 3000
+    D = L.PagedDims(B=1, Hq=Hq, Hkv=1, d=128, page=page, n_pages=200, max_pages=200, code="e4m3")
+    c = L.PagedCache(D)
+    k, v = torch.zeros(200 * page, 128, device="cuda"), 1 + torch.rand(200 * page, 128, device="cuda")
+    k[::32, 0], v[::32] = 16.0, 0.0
+    for name, x in (("k", k), ("v", v)):
+        getattr(c, name).copy_(x.to(torch.float8_e4m3fn).view(torch.uint8).view(200, page, 128)[None, :, None])
+    c.scale_k.fill_(1.0), c.scale_v.fill_(1.0)
+    c.page_table.copy_(torch.arange(200, device="cuda")), c.seq_len.fill_(T - t_q)
+    q = bf(1, t_q, Hq, 128)
+    for i, nats in enumerate((15.0, 16.0, 17.4, 20.0)):
+        q[:, :, i, 0] = nats * 128 ** 0.5 / 16
+    out = attn(D, c, q)
+    keys, vals = k.double(), v.to(torch.float8_e4m3fn).double()
+    pos = torch.arange(T - t_q, T, device="cuda")
+    for h in range(Hq):
+        assert float(out[0, :, h].abs().min()) > 0
+        U.check_rows(out[0, :, h], q[0, :, h], keys[:T], vals[:T], pos, T, L.Score(), h, 0, 2 * 2.0 ** -11, floor=2.0 ** -32)

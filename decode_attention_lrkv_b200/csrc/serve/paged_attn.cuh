@@ -417,9 +417,9 @@ __device__ __forceinline__ void join_rows(int n, const float* rec, int rows, int
   }
 }
 __device__ __forceinline__ void store_row4(lrkv_bf16* dst, const float4& o, float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(dst) = l > 0.f ? make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv))
-                                           : make_uint2(0u, 0u);
+  const float inv = 1.f / l;   // l = 0: the row saw nothing
+  *reinterpret_cast<uint2*>(dst) = l == 0.f ? make_uint2(0u, 0u)
+                                            : make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
 }
 
 // NB: blocks of 8 query rows; CODE: LRKV_CODE_*; PT: tokens of a tile on one page (16 or 32);
@@ -841,12 +841,12 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
         for (int j = 0; j < 2; ++j) {
           const int r = rho0 + 8 * nb + 2 * t4 + j;
           if (r >= rho1) continue;
-          const float inv = l[nb][j] > 0.f ? 1.f / l[nb][j] : 0.f;
+          const float inv = 1.f / l[nb][j];
           lrkv_bf16* dst = p.out + row_offset(p, at.b, h, r) + 2 * g8;
 #pragma unroll
           for (int dt = 0; dt < 8; ++dt)
             *reinterpret_cast<uint32_t*>(dst + 16 * dt) =
-                l[nb][j] > 0.f ? cvt_bf16x2(o[nb][dt][j] * inv, o[nb][dt][2 + j] * inv) : 0u;
+                l[nb][j] == 0.f ? 0u : cvt_bf16x2(o[nb][dt][j] * inv, o[nb][dt][2 + j] * inv);
         }
     } else {
       const int late = x < end ? 0 : 1;

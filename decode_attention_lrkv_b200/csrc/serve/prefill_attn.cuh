@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       tc5::fence_before_sync();
       mbar_arrive(&bars->p_full[x][it & 1]);
     }
-    // out = O / l; zeros for a row that saw nothing
+    // out = O / l; zeros for a row that saw nothing (l = 0: a row with a NaN has a NaN there)
     if (nt > 0 && ok)
       ok = __all_sync(0xffffffffu, wait_or_abort(&bars->s_full[x][(nt + 1) & 1], ((nt + 1) >> 1) & 1, abort_flag));
     if (ok && p.n_split > 1) {
@@ -477,10 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(rec + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
-      if (row < n_q) rec[kD] = nt > 0 ? m : -INFINITY, rec[kD + 1] = l;
+      // a row with NaN scores alone has no reference, but has seen keys: the join has to take its NaN
+      if (row < n_q) rec[kD] = nt == 0 ? -INFINITY : m == -INFINITY && l != 0.f ? 0.f : m, rec[kD + 1] = l;
     } else if (ok) {
       tc5::fence_after_sync();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = 1.f / l;
       lrkv_bf16* orow = p.out + b * p.os_b + row * p.os_t + h * p.os_h;
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            w[e] = l > 0.f ? cvt_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+            w[e] = l == 0.f ? 0u : cvt_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
 #pragma unroll
           for (int e = 0; e < 16; e += 8) {
             if (p.out32) {
@@ -547,9 +548,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
     l = fmaf(w, r[kD + 1], l);
     o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = 1.f / l;
   *reinterpret_cast<uint2*>(p.out + b * p.os_b + row * p.os_t + h * p.os_h + 4 * lane) =
-      l > 0.f ? make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+      l == 0.f ? make_uint2(0u, 0u) : make_uint2(cvt_bf16x2(o.x * inv, o.y * inv), cvt_bf16x2(o.z * inv, o.w * inv));
 }
 
 }  // namespace prefill

@@ -47,7 +47,8 @@ extern "C" {
  *     s = s - slopes[head] |i - j|             if slopes
  *     seen: max(first_key, i - window + 1) <= j <= max(i, prefix_end - 1)
  * and j < the sequence's length.  A row that sees nothing gives zeros.  Keys that
- * are not seen may hold anything, NaN included. */
+ * are not seen may hold anything, NaN included; a row whose query or seen keys hold a NaN
+ * gives NaN. */
 typedef struct {
   float scale;               /* >= 0 and finite; 0 stands for 1 / sqrt(d) */
   float softcap;             /* >= 0 and finite; 0: none */

@@ -8,7 +8,7 @@ import torch
 import decode_attention_lrkv_b200 as L
 from oracle import serve as R
 from tests import serve_testutil as U
-from tests.test_gpu_paged import attn, check
+from tests.test_gpu_paged import attn, check, make
 from tests.test_gpu_pages import contents, filled, host, random_state, same, set_state
 
 pytestmark = pytest.mark.gpu
@@ -171,3 +171,45 @@ def test_many_weights_far_below_the_largest_one(Hq, t_q, page):
     for h in range(Hq):
         assert float(out[0, :, h].abs().min()) > 0
         U.check_rows(out[0, :, h], q[0, :, h], keys[:T], vals[:T], pos, T, L.Score(), h, 0, 2 * 2.0 ** -11, floor=2.0 ** -32)
+
+
+@pytest.mark.parametrize("t_q,t_k", [(300, 300), (40, 6000)])    # the second one splits the keys
+@pytest.mark.parametrize("score", [dict(), dict(softcap=20.0), dict(window=80)], ids=str)
+def test_a_prefill_hands_nan_on(t_q, t_k, score):
+    """Rows with a NaN of their own, or that see a NaN key, are NaN; the others are as they were."""
+    q, k, v = U.normal(1, 1, t_q, 4, 128), U.normal(2, 1, t_k, 2, 128), U.normal(3, 1, t_k, 2, 128)
+    first = torch.zeros(1, t_q, dtype=torch.int32, device="cuda")
+    first[0, 9] = 10 ** 9                                      # a row that sees nothing, its query NaN
+    s = L.Score(first_key=first, **score)
+    want, got = torch.zeros_like(q), torch.zeros_like(q)
+    L.lrkv_prefill_attn(q, k, v, want, score=s)
+    at = t_k - 20                                              # seen by the last 20 rows (a window: by some)
+    q[0, 3, 1], q[0, 9], k[0, at, 0, 5] = float("nan"), float("nan"), float("nan")
+    L.lrkv_prefill_attn(q, k, v, got, score=s)
+    nan = torch.zeros(t_q, 4, dtype=torch.bool)
+    nan[3, 1] = True
+    nan[t_q - 20:, :2] = True                                  # heads 0 and 1 read kv head 0
+    nan = nan.cuda()
+    assert bool(got[0][nan].isnan().all()) and torch.equal(got[0][~nan], want[0][~nan])
+    assert bool((got[0, 9] == 0).all())
+    k[:] = float("nan")                                        # nothing but NaN
+    L.lrkv_prefill_attn(q, k, v, got, score=s)
+    keep = torch.arange(t_q, device="cuda") != 9
+    assert bool(got[0][keep].isnan().all()) and bool((got[0, 9] == 0).all())
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("lens,t_q", [([20, 3000], 3), ([5, 40], 9)])
+def test_the_paged_attention_hands_nan_on(lens, t_q, code):
+    D, c = make(2, 8, 2, 32, lens, code, room=t_q)
+    q = U.normal(1, 2, t_q, 8, 128)
+    first = torch.zeros(2, t_q, dtype=torch.int32, device="cuda")
+    first[:, 1] = 10 ** 9
+    s = L.Score(first_key=first)
+    want = attn(D, c, q, score=s)
+    nan = torch.zeros(2, t_q, 8, dtype=torch.bool, device="cuda")
+    nan[0, 0, 3] = nan[1, 2, 7] = nan[:, 1] = True
+    q[nan] = float("nan")
+    got = attn(D, c, q, score=s)
+    nan[:, 1] = False                                          # these see nothing
+    assert bool(got[nan].isnan().all()) and torch.equal(got[~nan], want[~nan]) and bool((got[:, 1] == 0).all())

@@ -42,7 +42,8 @@ inline ScoreConsts score_consts(const lrkv_score* s) {
   if (s) {
     c.scale = s->scale;
     c.softcap = s->softcap;
-    c.window = s->window;
+    // positions lie within 2^24 of 0: such a window hides nothing, and i - window + 1 has to stay in 32 bits
+    c.window = s->window > (1 << 25) ? 0 : s->window;
     c.slopes = s->slopes;
     c.first_key = s->first_key;
     c.prefix_end = s->prefix_end;

@@ -213,3 +213,18 @@ def test_the_paged_attention_hands_nan_on(lens, t_q, code):
     got = attn(D, c, q, score=s)
     nan[:, 1] = False                                          # these see nothing
     assert bool(got[nan].isnan().all()) and torch.equal(got[~nan], want[~nan]) and bool((got[:, 1] == 0).all())
+
+
+def test_windows_wider_than_any_sequence():
+    """The widest window hides nothing, in front of the first key too (more rows than keys)."""
+    q, k, v = U.normal(1, 2, 80, 4, 128), U.normal(2, 2, 60, 2, 128), U.normal(3, 2, 60, 2, 128)
+    end = torch.full((2, 80), 30, dtype=torch.int32, device="cuda")
+    for n in (2 ** 31 - 1, 2 ** 25 + 1, 2 ** 25, 2 ** 24):
+        for e in (end, None):
+            want, got = torch.zeros_like(q), torch.zeros_like(q)
+            L.lrkv_prefill_attn(q, k, v, want, score=L.Score(prefix_end=e))
+            L.lrkv_prefill_attn(q, k, v, got, score=L.Score(window=n, prefix_end=e))
+            assert torch.equal(got, want) and bool((want[:, :20] == 0).all()) == (e is None)
+    D, c = make(2, 4, 2, 32, [200, 3], "int8")
+    q = U.normal(4, 2, 2, 4, 128)
+    assert torch.equal(attn(D, c, q, score=L.Score(window=2 ** 31 - 1)), attn(D, c, q))

@@ -115,6 +115,7 @@ class Score(_Fields):
     prefix_end: torch.Tensor = None
 
     def __post_init__(self):
+        _int32(self.window, "window")
         plain = self.slopes is None and self.first_key is None and self.prefix_end is None
         object.__setattr__(self, "_struct", self.c() if plain else None)
         object.__setattr__(self, "_plain", ctypes.byref(self._struct) if plain else None)
@@ -143,8 +144,8 @@ class PagedDims(_Fields):
         object.__setattr__(self, "_at", ctypes.addressof(self._struct))
 
     def c(self):
-        return _PagedDims(self.B, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages, self.n_layers,
-                          CODES[self.code])
+        sizes = ("B", "Hq", "Hkv", "d", "page", "n_pages", "max_pages", "n_layers")
+        return _PagedDims(*(_int32(getattr(self, n), n) for n in sizes), CODES[self.code])
 
 
 class PagedCache:
@@ -197,6 +198,13 @@ class PagedCache:
 
     def nbytes(self):
         return sum(getattr(self, f).numel() * getattr(self, f).element_size() for f in self.FIELDS)
+
+
+def _int32(value, name):
+    """ctypes cuts a whole number to 32 bits without a word."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name}: {value} does not fit in 32 bits")
+    return value
 
 
 def _addr(t):
@@ -286,6 +294,8 @@ def _done(code, what, check):
 def _prefill_dims(q, k, v, out):
     B, t_q, Hq, d = q.shape
     _, t_k, Hkv, _ = k.shape
+    for x in (B, t_q, Hq, t_k, Hkv, d):
+        _int32(x, "a size of q or k")
     return _PrefillDims(B, Hq, Hkv, d, t_q, t_k, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3])
 
 
@@ -342,7 +352,7 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
 
 
 def lrkv_paged_workspace_size(dims, t_q=1):
-    return int(load_serve_library().lrkv_paged_workspace_size(dims._ref, int(t_q)))
+    return int(load_serve_library().lrkv_paged_workspace_size(dims._ref, _int32(int(t_q), "t_q")))
 
 
 def make_paged_workspace(dims, t_q=1, device="cuda"):
@@ -365,8 +375,8 @@ def lrkv_paged_append(dims, cache, layer, k_new, v_new, t_new_b=None, stream=Non
     _check(v_new, "v_new", shape, torch.bfloat16, device)
     _check_list(t_new_b, "t_new_b", dims.B, device)
     return _done(load_serve_library().lrkv_paged_append(
-        dims._ref, _cache_ref(dims, cache, device), layer, k_new.data_ptr(), v_new.data_ptr(), t_new, _addr(t_new_b),
-        _stream(stream, device)), "lrkv_paged_append", check)
+        dims._ref, _cache_ref(dims, cache, device), _int32(layer, "layer"), k_new.data_ptr(), v_new.data_ptr(), t_new,
+        _addr(t_new_b), _stream(stream, device)), "lrkv_paged_append", check)
 
 
 def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None, check=True):
@@ -382,8 +392,8 @@ def lrkv_paged_read(dims, cache, layer, first, count, k_out, v_out, stream=None,
     _check_list(first, "first", dims.B, device)
     _check_list(count, "count", dims.B, device)
     return _done(load_serve_library().lrkv_paged_read(
-        dims._ref, _cache_ref(dims, cache, device), layer, _addr(first), _addr(count), t_max, k_out.data_ptr(),
-        v_out.data_ptr(), _stream(stream, device)), "lrkv_paged_read", check)
+        dims._ref, _cache_ref(dims, cache, device), _int32(layer, "layer"), _addr(first), _addr(count), t_max,
+        k_out.data_ptr(), v_out.data_ptr(), _stream(stream, device)), "lrkv_paged_read", check)
 
 
 def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None, stream=None, check=True):
@@ -400,14 +410,15 @@ def lrkv_paged_attn(dims, cache, layer, q, out, t_q_b=None, score=None, ws=None,
     _check_score(score, dims.B, t_q, dims.Hq, device)
     n_ws = _check_ws(ws, device)
     return _done(load_serve_library().lrkv_paged_attn(
-        dims._ref, _cache_ref(dims, cache, device), layer, q.data_ptr(), t_q, _addr(t_q_b), _ref(score), out.data_ptr(),
-        _addr(ws), n_ws, _stream(stream, device)), "lrkv_paged_attn", check)
+        dims._ref, _cache_ref(dims, cache, device), _int32(layer, "layer"), q.data_ptr(), t_q, _addr(t_q_b),
+        _ref(score), out.data_ptr(), _addr(ws), n_ws, _stream(stream, device)), "lrkv_paged_attn", check)
 
 
 def _count_call(fn, name, dims, cache, t_new, t_new_b, stream, check):
     device = _device(cache.k, "cache")
     _check_list(t_new_b, "t_new_b", dims.B, device)
-    return _done(fn(dims._ref, _cache_ref(dims, cache, device), t_new, _addr(t_new_b), _stream(stream, device)), name, check)
+    return _done(fn(dims._ref, _cache_ref(dims, cache, device), _int32(t_new, "t_new"), _addr(t_new_b),
+                    _stream(stream, device)), name, check)
 
 
 def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True):
@@ -433,8 +444,8 @@ def _pair_call(fn, name, dims, cache, src, dst, ws, stream, check):
     _check_list(src, "src", n, device)
     _check_list(dst, "dst", n, device)
     n_ws = _check_ws(ws, device)
-    return _done(fn(dims._ref, _cache_ref(dims, cache, device), src.data_ptr(), dst.data_ptr(), n, _addr(ws), n_ws,
-                    _stream(stream, device)), name, check)
+    return _done(fn(dims._ref, _cache_ref(dims, cache, device), src.data_ptr(), dst.data_ptr(), _int32(n, "src"),
+                    _addr(ws), n_ws, _stream(stream, device)), name, check)
 
 
 def lrkv_pages_fork(dims, cache, src, dst, ws=None, stream=None, check=True):
@@ -460,8 +471,9 @@ def lrkv_pages_free(dims, cache, seqs, stream=None, check=True):
         return _done(code, "lrkv_pages_free", check)
     device, n = _device(cache.k, "cache"), seqs.numel()
     _check_list(seqs, "seqs", n, device)
-    return _done(load_serve_library().lrkv_pages_free(dims._ref, _cache_ref(dims, cache, device), seqs.data_ptr(), n,
-                                                      _stream(stream, device)), "lrkv_pages_free", check)
+    return _done(load_serve_library().lrkv_pages_free(
+        dims._ref, _cache_ref(dims, cache, device), seqs.data_ptr(), _int32(n, "seqs"), _stream(stream, device)),
+        "lrkv_pages_free", check)
 
 
 def lrkv_pages_compact(dims, cache, ws=None, stream=None, check=True):

@@ -9,9 +9,9 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 
-# These call the libraries with made-up addresses, which a host check has to refuse.  Where one
+# These call the libraries with addresses that are made up or the host's, which a check has to refuse.  Where one
 # does not, a kernel would be launched on them: no process that runs them may reach a GPU.
-MADE_UP_ADDRESSES = ("test_abi.py", "test_serve_abi.py", "test_serve_refusals.py")
+MADE_UP_ADDRESSES = ("test_abi.py", "test_serve_abi.py", "test_serve_binding.py")
 _without_gpu = {}    # module: the result of its run in a process of its own
 
 

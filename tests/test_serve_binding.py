@@ -50,3 +50,28 @@ def test_a_cache_keeps_its_shapes():
         L.PagedCache(D, device="cpu", keys=table)
     for other in (copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
         assert other.dims == D and all(torch.equal(getattr(other, n), getattr(c, n)) for n in c.FIELDS)
+
+
+def test_whole_numbers_that_do_not_fit_are_refused(monkeypatch):
+    """None of them is cut to 32 bits: 2^32 is no layer 0, and 2^32 + 1 tokens are not one."""
+    big = 2 ** 32 + 1
+    for name in ("B", "Hq", "Hkv", "n_pages", "max_pages", "n_layers"):
+        with pytest.raises(ValueError, match=f"{name}: .* 32 bits"):
+            small(**{name: big})
+    for kw in (dict(window=big), dict(window=big, slopes=torch.zeros(4))):
+        with pytest.raises(ValueError, match="window: .* 32 bits"):
+            L.Score(**kw)
+    D = small()
+    with pytest.raises(ValueError, match="t_q: .* 32 bits"):
+        L.lrkv_paged_workspace_size(D, big)
+    c = L.PagedCache(D, device="cpu")
+    monkeypatch.setattr(S, "_device", lambda t, name: -1)     # as if the host's tensors were on the device
+    monkeypatch.setattr(S, "_stream", lambda stream, device: None)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: L.lrkv_paged_append(D, c, big, bf(2, 1, 2, 128), bf(2, 1, 2, 128)),
+                 lambda: L.lrkv_paged_read(D, c, big, None, n, bf(2, 1, 2, 128), bf(2, 1, 2, 128)),
+                 lambda: L.lrkv_paged_attn(D, c, big, bf(2, 1, 4, 128), bf(2, 1, 4, 128)),
+                 lambda: L.lrkv_pages_reserve(D, c, big), lambda: L.lrkv_pages_advance(D, c, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()

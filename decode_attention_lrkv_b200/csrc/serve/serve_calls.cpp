@@ -289,7 +289,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) try {
     return slow();
   if (a[7] != Py_None) {
     const at::Tensor* t = tensor(a[7]);
-    if (!t || !on_device(*t, device)) return slow();
+    if (!t || !on_device(*t, device) || t->scalar_type() != at::kInt || !t->is_contiguous() || t->numel() < 1) return slow();
     status = t->data_ptr();
   }
   at::Tensor own;   // freed on return, for later work of the same stream

@@ -249,6 +249,15 @@ def _check_list(t, name, n, device):
         _check(t, name, (n,), torch.int32, device)
 
 
+def _check_status(t, device):
+    if t is None:
+        return
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < 1:
+        raise ValueError(f"dev_status: a contiguous int32 tensor of a word at least is needed, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device:
+        _wrong_device(t, "dev_status", device)
+
+
 def _check_ws(ws, device):
     if ws is None:
         return 0
@@ -337,8 +346,7 @@ def lrkv_prefill_attn(q, k, v, out, q_len=None, kv_len=None, score=None, dev_sta
     _check_list(q_len, "q_len", B, device)
     _check_list(kv_len, "kv_len", B, device)
     _check_score(score, B, t_q, Hq, device)
-    if dev_status is not None and dev_status.get_device() != device:
-        _wrong_device(dev_status, "dev_status", device)
+    _check_status(dev_status, device)
     n_ws = _check_ws(ws, device)
     lib, dims = load_serve_library(), ctypes.byref(_prefill_dims(q, k, v, out))
     if ws is None:

@@ -228,3 +228,11 @@ def test_windows_wider_than_any_sequence():
     D, c = make(2, 4, 2, 32, [200, 3], "int8")
     q = U.normal(4, 2, 2, 4, 128)
     assert torch.equal(attn(D, c, q, score=L.Score(window=2 ** 31 - 1)), attn(D, c, q))
+
+
+def test_a_status_word_of_another_type_is_refused():
+    q, k, v = bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128)
+    for bad in (torch.zeros(4, device="cuda"), torch.zeros(1, dtype=torch.uint8, device="cuda"), U.ints([])):
+        with pytest.raises(ValueError, match="dev_status"):
+            L.lrkv_prefill_attn(q, k, v, torch.zeros_like(q), dev_status=bad)
+    L.lrkv_prefill_attn(q, k, v, torch.zeros_like(q), dev_status=U.ints([0]))

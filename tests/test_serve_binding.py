@@ -75,3 +75,12 @@ def test_whole_numbers_that_do_not_fit_are_refused(monkeypatch):
                  lambda: L.lrkv_pages_reserve(D, c, big), lambda: L.lrkv_pages_advance(D, c, big)):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(4), torch.zeros(4, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32),
+                                 torch.zeros(4, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32).T], ids=str)
+def test_a_status_word_is_an_int32(bad, monkeypatch):
+    monkeypatch.setattr(S, "_device", lambda t, name: -1)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="dev_status"):
+        L.lrkv_prefill_attn(bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128), bf(1, 4, 4, 128), dev_status=bad)

@@ -15,6 +15,10 @@ namespace paged {
 constexpr int kPlanThreads = 1024, kMoveThreads = 256;
 constexpr int kMoveVec = 4;   // 16-byte pieces that a thread has in flight
 constexpr int kMoveBytes = kMoveThreads * kMoveVec * 16;
+// Entries of a list of sequences.  There are 65535 sequences at most, so a longer one names some of
+// them twice; to find those, an entry is compared with all before it (2^31 comparisons for such a
+// list, a few ms of the whole GPU; for 2^24 entries it would be minutes).
+constexpr int kMaxSeqList = 1 << 16;
 
 struct PageParams {
   lrkv_paged_dims D;
@@ -567,6 +571,7 @@ lrkv_status lrkv_pages_fork(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   PageParams p = {};
   lrkv_status st = list_call(dims, cache, src, dst, n, ws, ws_bytes, &p);
   if (st != LRKV_OK || n == 0) return st;
+  if (n > kMaxSeqList) return LRKV_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((st = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p)) != LRKV_OK) return st;
   return launch_pdl(fork_move_kernel, dim3(move_grid(*dims, n, n)), dim3(kMoveThreads), 0, s, p);
@@ -577,7 +582,7 @@ lrkv_status lrkv_pages_free(const lrkv_paged_dims* dims, const lrkv_paged_cache*
   const lrkv_status st = paged::check_all(dims, cache);
   if (st != LRKV_OK) return st;
   if (n < 0 || (n > 0 && !seqs)) return LRKV_ERR_INVALID_ARG;
-  if (n > (1 << 24)) return LRKV_ERR_UNSUPPORTED;
+  if (n > kMaxSeqList) return LRKV_ERR_UNSUPPORTED;
   if (!aligned16(seqs)) return LRKV_ERR_ALIGNMENT;
   if (n == 0) return LRKV_OK;
   PageParams p = {};

@@ -199,7 +199,8 @@ LRKV_API lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_pag
 /* ---- pages ------------------------------------------------------------------
  * Free pages are those with refs = 0; they are handed out lowest id first, in
  * the order of the sequences (or list entries) that ask.  A sequence's row of the
- * page table is filled from the front.  Lists have at most 2^24 entries.  ws: the
+ * page table is filled from the front.  Lists of sequences have at most 2^16 entries, lists of
+ * pages 2^24 (LRKV_ERR_UNSUPPORTED beyond).  ws: the
  * workspace of lrkv_paged_attn (any t_q). */
 
 /* Pages for t_new (or t_new_b[b]) more tokens of every sequence.  A sequence for

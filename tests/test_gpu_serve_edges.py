@@ -236,3 +236,19 @@ def test_a_status_word_of_another_type_is_refused():
         with pytest.raises(ValueError, match="dev_status"):
             L.lrkv_prefill_attn(q, k, v, torch.zeros_like(q), dev_status=bad)
     L.lrkv_prefill_attn(q, k, v, torch.zeros_like(q), dev_status=U.ints([0]))
+
+
+def test_the_longest_lists_of_sequences():
+    D, c, ws = filled(300, 16, 900, 6, n_layers=1, Hkv=1)
+    random_state(c, 1)
+    n, rng = 2 ** 16, random.Random(2)
+    pool, before = host(c), contents(c)
+    src, dst = [rng.randint(-1, 300) for _ in range(n)], [rng.randint(-1, 300) for _ in range(n)]
+    L.lrkv_pages_fork(D, c, U.ints(src), U.ints(dst), ws=ws)
+    pool.fork(src, dst)
+    same(c, pool, before)
+    before = contents(c)
+    seqs = [rng.randint(-1, 200) for _ in range(n)]
+    L.lrkv_pages_free(D, c, U.ints(seqs))
+    pool.free(seqs)
+    same(c, pool, before)

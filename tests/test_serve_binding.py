@@ -84,3 +84,16 @@ def test_a_status_word_is_an_int32(bad, monkeypatch):
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="dev_status"):
         L.lrkv_prefill_attn(bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128), bf(1, 4, 4, 128), dev_status=bad)
+
+
+def test_lists_of_sequences_end_where_comparing_them_would_take_long():
+    import ctypes
+    lib = L.load_serve_library()
+    at = 1 << 29                                              # an address that no refused call looks at
+    D = small().c()
+    C = S._PagedCache(*(at + (i << 24) for i in range(8)))
+    D, C = ctypes.byref(D), ctypes.byref(C)
+    for n in (2 ** 16 + 1, 2 ** 24):
+        assert lib.lrkv_pages_free(D, C, at, n, None) == 2, n
+        assert lib.lrkv_pages_fork(D, C, at, at, n, at, 1 << 40, None) == 2, n
+    assert lib.lrkv_pages_copy(D, C, at, at, 2 ** 24 + 1, at, 1 << 40, None) == 2

@@ -33,7 +33,7 @@ struct Library {
 bool bound = false;
 
 // Attribute names, made once.
-PyObject *s_at, *s_dims, *s_scale, *s_softcap, *s_window, *s_slopes, *s_first_key, *s_prefix_end;
+PyObject *s_at, *s_score_at, *s_dims, *s_scale, *s_softcap, *s_window, *s_slopes, *s_first_key, *s_prefix_end;
 PyObject* s_cache[8];
 
 struct Ref {   // an owned reference
@@ -129,7 +129,7 @@ bool real(PyObject* obj, PyObject* name, float* v) {
 bool score_of(PyObject* score, int64_t B, int64_t t_q, int64_t Hq, int device, lrkv_score* s, const lrkv_score** at) {
   *at = nullptr;
   if (score == Py_None) return true;
-  Ref plain(PyObject_GetAttr(score, s_at));
+  Ref plain(PyObject_GetAttr(score, s_score_at));
   if (!plain.o) return false;
   if (plain.o != Py_None) {
     *at = static_cast<const lrkv_score*>(PyLong_AsVoidPtr(plain.o));
@@ -331,7 +331,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serve_calls", nullptr, -1, method
 }  // namespace
 
 PyMODINIT_FUNC PyInit__serve_calls() {
-  s_at = PyUnicode_InternFromString("_at");
+  s_at = PyUnicode_InternFromString("_at");               // of PagedDims
+  s_score_at = PyUnicode_InternFromString("_score_at");   // of Score: another name, so that neither passes for the other
   s_dims = PyUnicode_InternFromString("dims");
   s_scale = PyUnicode_InternFromString("scale");
   s_softcap = PyUnicode_InternFromString("softcap");

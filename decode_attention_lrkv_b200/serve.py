@@ -119,7 +119,7 @@ class Score(_Fields):
         plain = self.slopes is None and self.first_key is None and self.prefix_end is None
         object.__setattr__(self, "_struct", self.c() if plain else None)
         object.__setattr__(self, "_plain", ctypes.byref(self._struct) if plain else None)
-        object.__setattr__(self, "_at", ctypes.addressof(self._struct) if plain else None)
+        object.__setattr__(self, "_score_at", ctypes.addressof(self._struct) if plain else None)
 
     def c(self):
         return _Score(self.scale, self.softcap, self.window, _addr(self.slopes), _addr(self.first_key),
@@ -234,7 +234,11 @@ def _device(t, name):
 
 
 def _check_score(score, B, t_q, Hq, device):
-    if score is None or score._plain is not None:
+    if score is None:
+        return
+    if not isinstance(score, Score):
+        raise TypeError(f"score: a Score is needed, got {type(score).__name__}")
+    if score._plain is not None:
         return
     if score.slopes is not None:
         _check(score.slopes, "slopes", (Hq,), torch.float32, device)

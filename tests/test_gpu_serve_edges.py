@@ -252,3 +252,12 @@ def test_the_longest_lists_of_sequences():
     L.lrkv_pages_free(D, c, U.ints(seqs))
     pool.free(seqs)
     same(c, pool, before)
+
+
+def test_dims_are_no_score():
+    D, c = make(2, 4, 2, 32, [5, 9], "int8")
+    q = U.normal(1, 2, 1, 4, 128)
+    with pytest.raises(TypeError, match="a Score is needed"):
+        attn(D, c, q, score=D)
+    with pytest.raises(TypeError, match="a Score is needed"):
+        L.lrkv_prefill_attn(q, q, q, torch.zeros_like(q), score=D)

@@ -97,3 +97,17 @@ def test_lists_of_sequences_end_where_comparing_them_would_take_long():
         assert lib.lrkv_pages_free(D, C, at, n, None) == 2, n
         assert lib.lrkv_pages_fork(D, C, at, at, n, at, 1 << 40, None) == 2, n
     assert lib.lrkv_pages_copy(D, C, at, at, 2 ** 24 + 1, at, 1 << 40, None) == 2
+
+
+def test_only_a_score_is_taken_for_one(monkeypatch):
+    """Dims hold the address of a struct as scores do: they must not be read as one."""
+    D = small()
+    assert not hasattr(D, "_score_at") and not hasattr(L.Score(), "_at")
+    c = L.PagedCache(D, device="cpu")
+    monkeypatch.setattr(S, "_device", lambda t, name: -1)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    for bad in (D, 3, "causal"):
+        with pytest.raises(TypeError, match="a Score is needed"):
+            L.lrkv_paged_attn(D, c, 0, bf(2, 1, 4, 128), bf(2, 1, 4, 128), score=bad)
+        with pytest.raises(TypeError, match="a Score is needed"):
+            L.lrkv_prefill_attn(bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128), bf(1, 4, 4, 128), score=bad)

@@ -7,15 +7,18 @@ Every csrc/*.cu (liblrkv.so, include/lrkv.h) and csrc/serve/*.cu
 (in parallel, into _build/), then each library's objects are linked with the
 static CUDA runtime, so the libraries carry no run-time path dependencies.
 _serve_calls.so, the Python binding's fast path, is compiled with g++ against
-torch's headers and Python's.
+torch's headers and Python's, and again when either of them changes; where that
+fails there is a warning, and the binding does without.
 """
 import concurrent.futures
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +30,7 @@ SERVE_CSRC = os.path.join(CSRC, "serve")
 SERVE_LIB = os.path.join(PKG, "liblrkv_serve.so")
 CALLS_SRC = os.path.join(SERVE_CSRC, "serve_calls.cpp")
 CALLS_LIB = os.path.join(PKG, "_serve_calls.so")
+CALLS_STAMP = os.path.join(OBJ, "serve_calls.made_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
@@ -73,8 +77,20 @@ def _calls_inputs():
     return [CALLS_SRC, os.path.join(INCLUDE, "lrkv.h"), os.path.join(INCLUDE, "lrkv_serve.h"), os.path.abspath(__file__)]
 
 
+def _calls_made_for():
+    """What _serve_calls.so is compiled against beside its sources."""
+    return f"torch {importlib.metadata.version('torch')}, Python {sys.version}"
+
+
+def _calls_current():
+    if not _newer(CALLS_LIB, _calls_inputs()) or not os.path.exists(CALLS_STAMP):
+        return False
+    with open(CALLS_STAMP) as f:
+        return f.read() == _calls_made_for()
+
+
 def up_to_date():
-    return _newer(LIB, _inputs()) and _newer(SERVE_LIB, _serve_inputs()) and _newer(CALLS_LIB, _calls_inputs())
+    return _newer(LIB, _inputs()) and _newer(SERVE_LIB, _serve_inputs()) and _calls_current()
 
 
 def _compile(src, extra):
@@ -95,6 +111,9 @@ def _link(objs, lib):
 
 def _build_calls():
     import torch
+    for old in (CALLS_STAMP, CALLS_LIB):   # what cannot be built again may not fit any more
+        if os.path.exists(old):
+            os.remove(old)
     home = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     tmp = CALLS_LIB + ".tmp"
@@ -107,6 +126,8 @@ def _build_calls():
     if r.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(tmp, CALLS_LIB)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_calls_made_for())
 
 
 def build(force=False, verbose=False, extra=()):
@@ -118,7 +139,7 @@ def build(force=False, verbose=False, extra=()):
     srcs = [s for _, part in todo for s in part]
     workers = max(1, min(len(srcs) + 1, os.cpu_count() or 1))
     with concurrent.futures.ThreadPoolExecutor(workers) as ex:
-        calls = ex.submit(_build_calls) if force or not _newer(CALLS_LIB, _calls_inputs()) else None
+        calls = ex.submit(_build_calls) if force or not _calls_current() else None
         results = dict(zip(srcs, ex.map(lambda s: _compile(s, list(extra)), srcs)))
     for obj, cmd, r in results.values():
         if verbose:
@@ -129,8 +150,8 @@ def build(force=False, verbose=False, extra=()):
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     for lib, part in todo:
         _link([results[s][0] for s in part], lib)
-    if calls is not None:
-        calls.result()
+    if calls is not None and (error := calls.exception()):
+        warnings.warn(f"_serve_calls.so was not built, the binding marshals its calls in Python: {error}", RuntimeWarning)
     return LIB
 
 

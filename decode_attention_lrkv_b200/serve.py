@@ -7,6 +7,7 @@ and types; the same names as in the C ABI are re-exported by the package.
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass, fields
 
 import torch
@@ -60,6 +61,13 @@ _SIGNATURES = {
 }
 
 
+class _InPython:
+    """In place of the calls in C++: every one is for the Python path."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
 def load_serve_library(path=None):
     """Load liblrkv_serve.so (built in-tree).  Raises if it has not been built."""
     global _lib, _calls
@@ -75,11 +83,14 @@ def load_serve_library(path=None):
     if path is None:
         try:
             from . import _serve_calls
-        except ImportError as e:
-            raise RuntimeError("_serve_calls.so is missing: build it with `python -m decode_attention_lrkv_b200.build`") from e
-        _serve_calls.bind([ctypes.cast(getattr(lib, "lrkv_" + n), _P).value for n in (
-            "prefill_workspace_size", "prefill_attn", "paged_append", "paged_read", "paged_attn", "pages_reserve",
-            "pages_advance", "pages_fork", "pages_copy", "pages_free", "pages_compact")])
+            _serve_calls.bind([ctypes.cast(getattr(lib, "lrkv_" + n), _P).value for n in (
+                "prefill_workspace_size", "prefill_attn", "paged_append", "paged_read", "paged_attn", "pages_reserve",
+                "pages_advance", "pages_fork", "pages_copy", "pages_free", "pages_compact")])
+        except (ImportError, ValueError) as e:   # missing, or built for another torch
+            warnings.warn(f"_serve_calls.so cannot be used ({e}): the calls are marshalled in Python, which takes "
+                          "several microseconds more of host time; build it with "
+                          "`python -m decode_attention_lrkv_b200.build`", RuntimeWarning, stacklevel=2)
+            _serve_calls = _InPython()
         _lib, _calls = lib, _serve_calls
     return lib
 

@@ -1,12 +1,18 @@
 """What the Python binding of the serving calls refuses by itself, without a GPU."""
 import copy
+import os
 import pickle
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import decode_attention_lrkv_b200 as L
+from decode_attention_lrkv_b200 import build
 from decode_attention_lrkv_b200 import serve as S
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def small(**kw):
@@ -111,3 +117,59 @@ def test_only_a_score_is_taken_for_one(monkeypatch):
             L.lrkv_paged_attn(D, c, 0, bf(2, 1, 4, 128), bf(2, 1, 4, 128), score=bad)
         with pytest.raises(TypeError, match="a Score is needed"):
             L.lrkv_prefill_attn(bf(1, 4, 4, 128), bf(1, 4, 2, 128), bf(1, 4, 2, 128), bf(1, 4, 4, 128), score=bad)
+
+
+def run(code):
+    return subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT,
+                          env={**os.environ, "CUDA_VISIBLE_DEVICES": ""})
+
+
+@pytest.mark.parametrize("error", ["ImportError('undefined symbol: of_another_torch')", "ModuleNotFoundError('no such file')"])
+def test_the_binding_does_without_its_fast_path(error):
+    """What keeps _serve_calls from loading is said, and the Python path does the work."""
+    r = run(f"""
+import sys, warnings
+import decode_attention_lrkv_b200 as L
+class Broken:
+    def find_spec(self, name, path=None, target=None):
+        if name.endswith('_serve_calls'):
+            raise {error}
+sys.meta_path.insert(0, Broken())
+with warnings.catch_warnings(record=True) as w:
+    warnings.simplefilter('always')
+    L.load_serve_library()
+print('warned:', *[str(x.message) for x in w])
+D = L.PagedDims(B=2, Hq=4, Hkv=2, d=128, page=16, n_pages=4, max_pages=2)
+print(L.lrkv_paged_workspace_size(D) > 0)
+try:
+    L.lrkv_pages_reserve(D, L.PagedCache(D, device='cpu'), 1)
+except ValueError as e:
+    print('refused:', e)
+""")
+    assert r.returncode == 0, r.stderr
+    assert error.split("'")[1] in r.stdout and "True" in r.stdout and "refused: cache" in r.stdout, r.stdout
+
+
+def test_the_fast_path_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    lib, stamp = tmp_path / "_serve_calls.so", tmp_path / "made_for"
+    monkeypatch.setattr(build, "CALLS_LIB", str(lib))
+    monkeypatch.setattr(build, "CALLS_STAMP", str(stamp))
+    assert not build._calls_current()
+    lib.write_bytes(b"")
+    assert not build._calls_current()
+    stamp.write_text(build._calls_made_for())
+    assert build._calls_current()
+    monkeypatch.setattr(build.importlib.metadata, "version", lambda name: "9.9")
+    assert not build._calls_current()
+
+
+def test_a_failed_build_of_the_fast_path_leaves_the_libraries(tmp_path, monkeypatch):
+    lib = tmp_path / "_serve_calls.so"
+    lib.write_bytes(b"of another torch")
+    monkeypatch.setattr(build, "CALLS_LIB", str(lib))
+    monkeypatch.setattr(build, "CALLS_STAMP", str(tmp_path / "made_for"))
+    monkeypatch.setattr(build, "CALLS_SRC", str(tmp_path / "missing.cpp"))
+    monkeypatch.setattr(build, "_calls_inputs", lambda: [str(lib)])
+    with pytest.warns(RuntimeWarning, match="marshals its calls in Python"):
+        assert build.build() == build.LIB
+    assert not lib.exists()

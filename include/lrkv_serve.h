@@ -145,13 +145,15 @@ typedef struct {
  * Per page and head, with Q = 127 or 448 and x the new elements on it (an
  * infinity counts as the largest finite bf16, a NaN as 0), all steps in fp32
  * with IEEE rounding:
- *     s   = max(scale of the page's earlier tokens, max|x| / Q)
+ *     s   = max(scale of the page, max|x| / Q)   (0 for a page that starts with this call)
  *     s   = 0 if s < 2^-100
  *     inv = 1 / s  (0 if s = 0)
  *     code = x inv, rounded to the code's type (nearest, ties to even), in [-Q, Q]
  * and where s has grown, the codes already on the page are rounded once more:
  *     code = round(code (s_before inv)).
- * A page that starts with this call takes no account of what it held before.
+ * A page that starts with this call takes no account of what it held before.  Until then its
+ * scale covers all that was appended to it, drafted tokens that were never advanced over
+ * included: their effect on the scale, and on the codes that were rounded to it, stays.
  * Positions past the page table are dropped (LRKV_DEV_SEQ_OVERFLOW), as are
  * tokens whose table entry is no page (LRKV_DEV_BAD_PAGE). */
 LRKV_API lrkv_status lrkv_paged_append(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,

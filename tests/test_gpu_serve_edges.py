@@ -8,7 +8,8 @@ import torch
 import decode_attention_lrkv_b200 as L
 from oracle import serve as R
 from tests import serve_testutil as U
-from tests.test_gpu_paged import attn, check, make
+from tests.test_gpu_paged import attn, check, make, mirror_append
+from tests.test_gpu_paged import same as same_codes
 from tests.test_gpu_pages import contents, filled, host, random_state, same, set_state
 
 pytestmark = pytest.mark.gpu
@@ -261,3 +262,33 @@ def test_dims_are_no_score():
         attn(D, c, q, score=D)
     with pytest.raises(TypeError, match="a Score is needed"):
         L.lrkv_prefill_attn(q, q, q, torch.zeros_like(q), score=D)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_rejected_drafts_leave_their_mark_on_a_page_that_goes_on(page, code):
+    """Five drafted tokens, the last three loud; two are accepted and others appended over the rest.
+    The page's scale stays what the loud ones made it, but a page that starts anew forgets them."""
+    lens = [page + 4, page, 2 * page - 3]                   # on a page, at its start, over its end
+    D, c = make(3, 2, 2, page, lens, code, room=12)
+    before = c.scale_k.clone()
+    host = {n: getattr(c, n).cpu().clone() for n in ("k", "v", "scale_k", "scale_v")}
+
+    def append(seed, t, loud):
+        k, v = U.normal(seed, 3, t, 2, 128), U.normal(seed + 1, 3, t, 2, 128)
+        k[:, 2:] *= loud
+        for b in range(3):
+            mirror_append(D, host, 0, {"k": k[b].cpu(), "v": v[b].cpu()}, int(c.seq_len[b]), t, c.page_table[b].cpu())
+        L.lrkv_paged_append(D, c, 0, k, v)
+        same_codes(D, c, host)
+
+    append(1, 5, 50.0)
+    loud = c.scale_k.clone()
+    c.seq_len += U.ints([2, 0, 3])                            # none of the second one's is accepted
+    append(3, 3, 1.0)
+    at = [int(c.page_table[b, 1]) for b in range(3)]
+    assert torch.equal(c.scale_k[0, at[0]], loud[0, at[0]]) and bool((loud[0, at[0]] > before[0, at[0]]).all())
+    assert bool((c.scale_k[0, at[1]] < loud[0, at[1]]).all())
+    over = int(c.page_table[2, 2])                            # its first page ends with three accepted tokens
+    assert bool((c.scale_k[0, over] < loud[0, over]).all())
+    check(attn(D, c, U.normal(9, 3, 3, 2, 128)), D, c, U.normal(9, 3, 3, 2, 128))

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kMoveThreads) advance_kernel(const __grid_cons
   const int end = (stop + p.D.page - 1) / p.D.page;
   int hole = end;
   if (stop > len)
-#pragma unroll 4
+#pragma unroll 16
     for (int s = len / p.D.page + lane; s < end; s += 32)
       if (!in_range(row[s], p.D.n_pages)) hole = min(hole, s);
   hole = __reduce_min_sync(0xffffffffu, hole);

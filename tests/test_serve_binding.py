@@ -49,6 +49,8 @@ def test_a_cache_keeps_its_shapes():
             setattr(c, name, bad)
     with pytest.raises(AttributeError, match="dims"):
         c.dims = small(max_pages=9)
+    for mine in (1, 2):                                        # what a program adds is its own
+        c.mine = mine
     table = torch.full((2, 2), -1, dtype=torch.int32)
     c.page_table = table
     assert c.page_table is table and c.c().page_table == table.data_ptr()

@@ -195,10 +195,9 @@ class PagedCache:
         # the calls take the tensors' addresses, and the sizes from dims
         if name in self.FIELDS:
             _check(value, name, *self._shapes[name])
-            other = next((t for f in self.FIELDS if f != name and (t := self.__dict__.get(f)) is not None), value)
-            if value.device != other.device:
-                raise ValueError(f"{name}: the cache's other tensors are on {other.device}, this one is on "
-                                 f"{value.device}")
+            device = self.__dict__.setdefault("_device", value.device)   # that of the first one
+            if value.device != device:
+                raise ValueError(f"{name}: the cache's other tensors are on {device}, this one is on {value.device}")
         elif name in ("dims", "_shapes") and name in self.__dict__:
             raise AttributeError(f"a PagedCache's {name} cannot be replaced")
         object.__setattr__(self, name, value)

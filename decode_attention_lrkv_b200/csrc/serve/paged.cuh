@@ -127,9 +127,10 @@ struct PagedWs {
 };
 
 // Rows of one kv head (g t_q) in blocks, evenly, each padded to 8.  A block reads the cache
-// once: of up to 32 rows where a layer's cache is larger than L2 (100 tiles of 32 tokens for
-// every SM, 121 MB), of up to 8 where it fits, as the kernel for 8 rows has twice the warps and
-// less to fetch and join.  Measured with 20 rows: 7 sequences of 2500 to 5000 tokens 50 us in
+// once: of up to 32 rows where a layer's page tables have room for more than L2 holds (100 tiles
+// of 32 tokens for every SM, 121 MB), of up to 8 where they do not, as the kernel for 8 rows has
+// twice the warps and less to fetch and join.  (The lengths lie on the device: a table with
+// room for a long context takes the large blocks while its sequences are short, too.)  Measured with 20 rows: 7 sequences of 2500 to 5000 tokens 50 us in
 // blocks of 8, 58 us in one; of 20000 to 40000 tokens 209 and 166 us.
 inline PagedWs paged_ws(const lrkv_paged_dims& D, int t_q) {
   PagedWs L;

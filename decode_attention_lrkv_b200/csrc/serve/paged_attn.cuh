@@ -4,8 +4,9 @@
 // p_ij = exp(s_ij - m_i), s_ij the modified scores of (q_i . c_k,j) s_k(j), with codes c
 // and the scale s of the page that j lies on.
 //
-// Bound: memory (2 d bytes a token and kv head, read once).  The keys of all
-// (sequence, kv head, block of up to 32 query rows) are cut into tiles of 32 tokens
+// Bound: memory (2 d bytes a token and kv head, read once for each block of query rows:
+// of 8 rows, or of up to 32 where the page tables have room for more than L2 holds).  The keys
+// of all (sequence, kv head, block of query rows) are cut into tiles of 32 tokens
 // and numbered; every warp of the grid takes an equal, contiguous run of tiles, so
 // ragged lengths, few long sequences and many short ones all fill the SMs alike.
 // A warp works alone: one thread of it brings tiles in by TMA (128-byte swizzle, a ring of
@@ -136,7 +137,8 @@ struct Place {
   int seg;               // number of the segment's first tile
 };
 
-// a / b for 0 <= a < 2^31 and a quotient below 2^22: the fp32 quotient is off by one at most.
+// a / b for 0 <= a < 2^31 and a quotient below 2^20 (kv heads times row blocks: 65535 x 16, or
+// 14800 x 64): the fp32 quotient is off by one at most.
 __device__ __forceinline__ int div_small(int a, int b, float inv_b) {
   int q = (int)((float)a * inv_b);
   const int r = a - q * b;
@@ -189,7 +191,8 @@ struct Index {
   }
 };
 
-// x tiles cut into n equal runs: run i is [start(i), start(i + 1)).  n < 2^11.
+// x tiles cut into n equal runs: run i is [start(i), start(i + 1)).  n <= 16 for every SM, below
+// 2^12, so that rest * i < n^2 < 2^24 is exact in fp32.
 struct Runs {
   int n, quot, rest;
   float inv_n, per_tile;   // 1 / n; runs per tile, nearly

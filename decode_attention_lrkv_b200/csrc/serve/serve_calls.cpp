@@ -1,5 +1,6 @@
-// The calls of serve.py whose arguments are as they should be, marshalled in C++: 1 us less
-// than 1 us of host time a call where ctypes and the checks in Python take 5 to 10.
+// The calls of serve.py whose arguments are as they should be, marshalled in C++: 0.5 us of
+// host time a call up to its launch, where ctypes and the checks in Python take 3 to 7 (with
+// the launch 3.2 to 3.6 us against 7.3 to 8.5).
 //
 // A function returns the library's status, or -1 where something is out of the ordinary (a
 // tensor of another shape, type, device or layout, an explicit stream, a subclass of Tensor):

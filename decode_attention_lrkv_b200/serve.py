@@ -454,7 +454,7 @@ def lrkv_pages_reserve(dims, cache, t_new, t_new_b=None, stream=None, check=True
 
 
 def lrkv_pages_advance(dims, cache, t_new, t_new_b=None, stream=None, check=True):
-    """seq_len += t_new (or t_new_b)."""
+    """seq_len += t_new (or t_new_b), up to the first token that has no page."""
     code = _fast().counts(1, dims, cache, t_new, t_new_b, stream)
     if code >= 0:
         return _done(code, "lrkv_pages_advance", check)

@@ -48,14 +48,14 @@ extern "C" {
  *     seen: max(first_key, i - window + 1) <= j <= max(i, prefix_end - 1)
  * and j < the sequence's length.  A row that sees nothing gives zeros.  Keys that
  * are not seen may hold anything, NaN included; a row whose query or seen keys hold a NaN
- * gives NaN. */
+ * gives NaN.  For what may lie in values that are not seen, see each call. */
 typedef struct {
   float scale;               /* >= 0 and finite; 0 stands for 1 / sqrt(d) */
   float softcap;             /* >= 0 and finite; 0: none */
   int32_t window;            /* >= 0; 0: none */
   const float* slopes;       /* nullable [Hq]: distance bias (ALiBi), finite */
   const int32_t* first_key;  /* nullable [B][t_q]: the first key a row sees (the start of its
-                                document); past the row's position: it sees nothing */
+                                document); past the last one it may see: it sees nothing */
   const int32_t* prefix_end; /* nullable [B][t_q]: rows see every key below this, later
                                 ones included (a bidirectional prefix); 0: causal */
 } lrkv_score;
@@ -162,7 +162,7 @@ LRKV_API lrkv_status lrkv_paged_append(const lrkv_paged_dims* dims, const lrkv_p
                                        const int32_t* t_new_b, void* stream);
 
 /* Reads positions first[b] .. first[b] + count[b] - 1 of `layer` back as bf16
- * (code * scale, rounded once): the keys and values that a later chunk of a prompt
+ * (code * scale, rounded to fp32 and then to bf16): the keys and values that a later chunk of a prompt
  * attends to with lrkv_prefill_attn.
  * first: nullable [B] int32 (null: 0); count: [B] int32, clamped into [0, t_max].
  * k_out, v_out: [B][t_max][Hkv][d] bf16; rows at or past count[b], and rows
@@ -183,15 +183,18 @@ LRKV_API lrkv_status lrkv_paged_read(const lrkv_paged_dims* dims, const lrkv_pag
  *   past it are left as they were.
  * t_q: 1 .. 64.
  * ws: lrkv_paged_workspace_size(dims, t_q) bytes (for this t_q or a larger one),
- *   zero-filled once; the calls leave it as they need it.  One workspace serves one stream of calls (two captured
- *   graphs that may run at the same time need one each).
+ *   zero-filled once; the calls leave it as they need it.  A workspace belongs to one
+ *   lrkv_paged_dims (another lays it out in another way) and serves one stream of calls (two
+ *   captured graphs that may run at the same time need one each).
  * LRKV_ERR_UNSUPPORTED for a pool of 2^31 rows of codes or more, or a page table with
  *   room for 2^31 tiles of 32 tokens over all sequences, kv heads and blocks of query rows.
  * Logits and softmax in fp32; queries and weights enter the products as f16
  * (queries scaled by a power of two: exact up to 2^-28 of the row's largest
  * element; weights rounded to 11 bits down to 2^-21 of the row's largest, to steps of at
  * most 2^-31 of it below that; the sum that divides them is not rounded).  int8 codes
- * enter the fp32 sums with 128 added, which is taken off again. */
+ * enter the fp32 sums with 128 added, which is taken off again.  A value that a mask hides
+ * enters with weight zero and has to be finite (the e4m3 codes 0x7f and 0xff are NaN;
+ * lrkv_paged_append writes neither). */
 LRKV_API size_t lrkv_paged_workspace_size(const lrkv_paged_dims* dims, int32_t t_q);
 LRKV_API lrkv_status lrkv_paged_attn(const lrkv_paged_dims* dims, const lrkv_paged_cache* cache,
                                      int32_t layer, const lrkv_bf16* q, int32_t t_q,

@@ -36,11 +36,11 @@ namespace paged {
 
 constexpr int kTile = 32;                // tokens
 constexpr int kUnitBytes = kTile * kD;   // codes of a tile's keys, or of its values
-constexpr float kLazyMax = 8.f;          // rescale when a maximum grows by more (log2)
-// Weights are formed 2^7 times as large, up to 2^15, the top of f16's range: its smallest step is
-// then 2^-31 of the reference's weight.  (Without it, weights below 2^-25 became zero in the
-// products and still counted in the sum that divides them.)
-constexpr float kLift = 7.f, kUnlift = 1.f / 128.f;
+// The reference of a row's weights is set 7 below its maximum and moves when the maximum is more
+// than 15 above it (log2): weights reach 2^15, the top of f16's range, and its smallest step is
+// 2^-31 of the largest one's.  (With the maximum as the reference, weights below 2^-25 became zero
+// in the products and still counted in the sum that divides them.)
+constexpr float kLift = 7.f, kLazyMax = 15.f, kUnlift = 1.f / 128.f;
 
 struct AttnParams {
   CUtensorMap map_k, map_v;   // codes as rows of 128 bytes; box {128, min(page, 32)}
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
           const float mx0 = fmaxf(s[nb][0][j], s[nb][0][2 + j]), mx1 = fmaxf(s[nb][1][j], s[nb][1][2 + j]);
           if (PT == 16) mx[nb][j] = fmaxf(mx0 * f[nb][0][j], mx1 * f[nb][PT == 16 ? 1 : 0][j]);
           else mx[nb][j] = fmaxf(mx0, mx1) * f[nb][0][j];
-          grow |= mx[nb][j] > m[nb][j] + kLazyMax;
+          grow |= mx[nb][j] - m[nb][j] > kLazyMax;   // (m + kLazyMax is rounded where m is large)
         }
       }
       if (__any_sync(0xffffffffu, grow)) {
@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            const float m_new = fmaxf(m[nb][j], v);
+            const float m_new = fmaxf(m[nb][j], v - kLift);
             const float r = m_new == -INFINITY ? 1.f : ex2(m[nb][j] - m_new);
             m[nb][j] = m_new;
             l[nb][j] *= r;
@@ -764,8 +764,7 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
       uint32_t pf[NB][2][2];   // weights as B fragments
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const float ref0 = (m[nb][0] == -INFINITY ? 0.f : m[nb][0]) - kLift;
-        const float ref1 = (m[nb][1] == -INFINITY ? 0.f : m[nb][1]) - kLift;
+        const float ref0 = m[nb][0] == -INFINITY ? 0.f : m[nb][0], ref1 = m[nb][1] == -INFINITY ? 0.f : m[nb][1];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -790,7 +789,8 @@ __global__ void __launch_bounds__(AttnConfig<NB>::kThreads, 1) attn_kernel(const
 
       if (!wait_unit()) break;
       unsigned char* vt = ring + slot * kUnitBytes;
-      // results: e4m3 in plain units; int8 in 2^-17, which the sums of weights are brought to as well
+      // units of the results, to which the sums of weights are brought as well: 2^-7 (so that large
+      // values find room for lifted weights), of int8 codes 2^-24
       constexpr float kValue = kInt ? 1.f : kUnlift;
       const float sv0 = sh.scale[warp][slot][0] * kValue, sv1 = PT == 16 ? sh.scale[warp][slot][1] * kValue : sv0;
       if (!kInt && gone) {   // what lies there may be a NaN, which a zero weight keeps: clear those rows

@@ -117,7 +117,8 @@ typedef struct {
 
 /* One pool for all layers, one page table and one length per sequence: a page id
  * stands for the same tokens in every layer.  A page holds `page` tokens of every
- * kv head; its codes of one head share one scale: value = code * scale. */
+ * kv head; its codes of one head share one scale: value = code * scale.  Scales are 0 or
+ * 2^-100 and more, as lrkv_paged_append makes them. */
 typedef struct {
   void* k;             /* [n_layers][n_pages][Hkv][page][d] bytes: codes */
   void* v;             /* likewise */

@@ -8,7 +8,7 @@ import torch
 import decode_attention_lrkv_b200 as L
 from oracle import serve as R
 from tests import serve_testutil as U
-from tests.test_gpu_paged import attn, check, make, mirror_append
+from tests.test_gpu_paged import attn, check, make, mirror_append, values
 from tests.test_gpu_paged import same as same_codes
 from tests.test_gpu_pages import contents, filled, host, random_state, same, set_state
 
@@ -292,3 +292,26 @@ def test_rejected_drafts_leave_their_mark_on_a_page_that_goes_on(page, code):
     over = int(c.page_table[2, 2])                            # its first page ends with three accepted tokens
     assert bool((c.scale_k[0, over] < loud[0, over]).all())
     check(attn(D, c, U.normal(9, 3, 3, 2, 128)), D, c, U.normal(9, 3, 3, 2, 128))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_scores_past_what_fp32_counts_singly(code):
+    """Scores of some 10^8, where a step of fp32 is 8 or more: a key far above the others, wherever
+    it lies, is the output, and equal scores weigh the same on both sides of such a key."""
+    D, c = make(1, 4, 1, 32, [3000], code)
+    c.scale_v.fill_(1 / 64), c.scale_k.fill_(1.0)
+    for top in (5, 1500, 2999):
+        k = torch.zeros(D.max_pages * 32, 128, device="cuda")
+        k[:, 0], k[top, 0] = 32.0, 64.0
+        kk = k.to(torch.int8) if code == "int8" else k.to(torch.float8_e4m3fn)
+        c.k[0, c.page_table[0].long(), 0] = kk.view(torch.uint8).view(D.max_pages, 32, 128)
+        q = bf(1, 1, 4, 128)
+        q[..., 0] = torch.tensor([2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 27], device="cuda")
+        out = attn(D, c, q)
+        v = values(c, "v", 0, 0, 0, 3001)
+        assert torch.equal(out[0, 0], v[top].to(torch.bfloat16).expand(4, 128))
+    c.k[0, c.page_table[0].long(), 0] = 32 if code == "int8" else 0x60          # 32 as e4m3
+    out = attn(D, c, bf(1, 1, 4, 128) + torch.tensor([2.0 ** 24] + [0.0] * 127, device="cuda").bfloat16())
+    mean = v.mean(0)
+    # equal weights: a rounding of them is the same for all; the sums are off by 2^-8 of a half code step
+    assert bool(((out[0, 0].double() - mean).abs() <= U.U * mean.abs() + 2.0 ** -9 * v.abs().mean(0)).all())

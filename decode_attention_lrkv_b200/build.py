@@ -79,7 +79,12 @@ def _calls_inputs():
 
 def _calls_made_for():
     """What _serve_calls.so is compiled against beside its sources."""
-    return f"torch {importlib.metadata.version('torch')}, Python {sys.version}"
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # a source tree
+        import torch as module
+        torch = module.__version__
+    return f"torch {torch}, Python {sys.version}"
 
 
 def _calls_current():

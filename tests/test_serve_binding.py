@@ -165,6 +165,12 @@ def test_the_fast_path_is_built_again_for_another_torch(tmp_path, monkeypatch):
     assert not build._calls_current()
 
 
+def test_the_fast_path_that_was_built_is_used():
+    build.build()
+    S.load_serve_library()
+    assert not build._calls_current() or not isinstance(S._calls, S._InPython)
+
+
 def test_a_failed_build_of_the_fast_path_leaves_the_libraries(tmp_path, monkeypatch):
     lib = tmp_path / "_serve_calls.so"
     lib.write_bytes(b"of another torch")
